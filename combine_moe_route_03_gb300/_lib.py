@@ -22,6 +22,8 @@ GEMM_GATEUP_SWIGLU, GEMM_DOWN = 0, 1
 FMT_FP8, FMT_BF16, FMT_FP8_F32 = 0, 1, 2
 SCALE_UE8M0, SCALE_F32 = 0, 1   # moe_gemm_args.scale_fmt / moe_layer.scale_fmt
 
+TYPE_BF16, TYPE_F16, TYPE_F32 = 0, 1, 2
+
 _c_int, _c_i64, _c_sz, _vp, _f = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
 
 
@@ -81,6 +83,38 @@ class Layer(ctypes.Structure):
                                ("fuse_combine", _c_int), ("src_of", _vp), ("pending", _vp),
                                ("W2_sf_t224", _vp)]
 
+class Segments(ctypes.Structure):
+    _fields_ = [("counts", _vp), ("E", _c_int), ("align", _c_int), ("cap", _c_int),
+                ("rows", _c_i64)]
+
+
+class GgemmArgs(ctypes.Structure):
+    _fields_ = [("seg", Segments), ("n", _c_int), ("k", _c_int), ("trans", _c_int),
+                ("type", _c_int), ("x", _vp), ("w", _vp), ("out", _vp), ("status", _vp),
+                ("num_sms", _c_int)]
+
+
+class WgradArgs(ctypes.Structure):
+    _fields_ = [("seg", Segments), ("n", _c_int), ("k", _c_int), ("type", _c_int),
+                ("out_type", _c_int), ("accumulate", _c_int), ("dy", _vp), ("x", _vp),
+                ("out", _vp), ("status", _vp), ("num_sms", _c_int)]
+
+
+class SwigluArgs(ctypes.Structure):
+    _fields_ = [("seg", Segments), ("I", _c_int), ("type", _c_int), ("gu", _vp), ("dh", _vp),
+                ("row_w", _vp), ("out", _vp), ("drow_w", _vp), ("status", _vp)]
+
+
+class AdamwCfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+        ("step", _c_i64), ("state_bits", _c_int), ("grad_scale", _vp)]
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [("n", _c_i64), ("p", _vp), ("g", _vp), ("copy", _vp), ("m", _vp), ("v", _vp),
+                ("m_scale", _vp), ("r_scale", _vp), ("g_type", _c_int), ("copy_type", _c_int)]
+
+
 LAYER_EVENTS = 6
 STAGES = ("route", "dispatch", "gateup", "down", "combine")
 
@@ -105,6 +139,13 @@ SIGNATURES = {
     "moe_pack_weight_scales_tiled": (_c_int, [_c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
     "moe_fused_combine_prep": (_c_int, [ctypes.POINTER(FusedCombine), _c_int, _vp]),
     "moe_combine": (_c_int, [ctypes.POINTER(CombineCfg), _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_grouped_gemm": (_c_int, [ctypes.POINTER(GgemmArgs), _vp]),
+    "moe_grouped_wgrad": (_c_int, [ctypes.POINTER(WgradArgs), _vp]),
+    "moe_swiglu": (_c_int, [ctypes.POINTER(SwigluArgs), _vp]),
+    "moe_swiglu_backward": (_c_int, [ctypes.POINTER(SwigluArgs), _vp]),
+    "moe_adamw": (_c_int, [ctypes.POINTER(AdamwCfg), ctypes.POINTER(AdamwTensor), _c_int, _vp]),
+    "moe_adamw_decode": (_c_int, [_c_i64] + [_vp] * 7),
+    "moe_adamw_encode": (_c_int, [_c_i64] + [_vp] * 7),
     "moe_read_status": (_c_int, [_vp, _vp]),
     "moe_last_cuda_error": (_c_int, []),
     "moe_num_sms": (_c_int, []),

@@ -12,14 +12,16 @@ import torch
 
 from . import _lib
 from ._lib import (FMT_BF16, FMT_FP8, FMT_FP8_F32, GEMM_DOWN, GEMM_GATEUP_SWIGLU, SCALE_F32,
-                   SCALE_UE8M0, CombineCfg, DispatchCfg, EplbCfg, FusedCombine, GemmArgs, Layer,
-                   RouteCfg, check, load, ptr, stream_ptr)
+                   SCALE_UE8M0, AdamwCfg, AdamwTensor, CombineCfg, DispatchCfg, EplbCfg,
+                   FusedCombine, GemmArgs, GgemmArgs, Layer, RouteCfg, Segments, SwigluArgs,
+                   WgradArgs, check, load, ptr, stream_ptr)
 from .configs import MASKED, MoEConfig
 
 __all__ = ["route", "eplb_build_map", "eplb_plan", "check_eplb_map", "EplbRecorder", "dispatch", "dispatch_sizes", "pack_weight_scales",
            "grouped_gemm_fp8", "combine", "read_status", "new_status", "MoELayer",
            "FMT_FP8", "FMT_BF16", "FMT_FP8_F32", "SCALE_UE8M0", "SCALE_F32", "GEMM_GATEUP_SWIGLU",
-           "GEMM_DOWN", "num_sms", "scale_bytes", "weight_scales_f32"]
+           "GEMM_DOWN", "num_sms", "scale_bytes", "weight_scales_f32",
+           "grouped_gemm", "grouped_wgrad", "swiglu", "swiglu_backward", "AdamW"]
 
 
 def num_sms() -> int:
@@ -367,6 +369,230 @@ def combine(Y: torch.Tensor, row_of: torch.Tensor, topk_w: torch.Tensor,
     check(load().moe_combine(ctypes.byref(cc), ptr(Y), ptr(row_of), ptr(topk_w), ptr(shared),
                              ptr(out), ptr(st), _ordered(stream, st)), "moe_combine")
     return out
+
+
+_TYPES = {torch.bfloat16: _lib.TYPE_BF16, torch.float16: _lib.TYPE_F16,
+          torch.float32: _lib.TYPE_F32}
+_HALF = (torch.bfloat16, torch.float16)
+
+
+def _segments(counts: torch.Tensor | None, align: int, cap: int, rows: int) -> Segments:
+    if counts is None:
+        return Segments(None, 0, 1, 0, rows)
+    _expect(counts, "counts", (torch.int32,), (None,))
+    return Segments(ptr(counts), counts.numel(), align, cap, rows)
+
+
+def grouped_gemm(x: torch.Tensor, w: torch.Tensor, counts: torch.Tensor, trans: bool = False,
+                 align: int = 1, cap: int = 0, out: torch.Tensor | None = None,
+                 num_sms_: int = 0, status: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """moe_grouped_gemm: rows x of each expert's segment times w bf16 / fp16 [E][n][k]:
+    x [rows][k] -> out [rows][n], or with ``trans`` x [rows][n] -> out [rows][k].
+    counts int32 [E]: rows of each expert; align / cap: where the segments start
+    (align 128: a contiguous dispatch, 1: packed rows; cap: a masked dispatch).  Rows
+    outside the segments are not written."""
+    _expect(w, "w", _HALF, (None, None, None))
+    E, n, k = w.shape
+    red, cols = (n, k) if trans else (k, n)
+    _expect(x, "x", (w.dtype,), (None, red))
+    _expect(counts, "counts", (torch.int32,), (E,))
+    rows = x.shape[0]
+    if out is None:
+        out = torch.empty((rows, cols), dtype=w.dtype, device=x.device)
+    else:
+        _expect(out, "out", (w.dtype,), (rows, cols))
+    st = status if status is not None else new_status(x.device)
+    a = GgemmArgs(_segments(counts, align, cap, rows), n, k, int(trans), _TYPES[w.dtype], ptr(x),
+                  ptr(w), ptr(out), ptr(st), num_sms_)
+    check(load().moe_grouped_gemm(ctypes.byref(a), _ordered(stream, x, w, counts, out, st)),
+          "moe_grouped_gemm")
+    return out
+
+
+def grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, counts: torch.Tensor, align: int = 1,
+                  cap: int = 0, out: torch.Tensor | None = None,
+                  out_dtype: torch.dtype | None = None, accumulate: bool = False,
+                  num_sms_: int = 0, status: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """moe_grouped_wgrad: dy [rows][n], x [rows][k] -> out [E][n][k], the gradient of
+    grouped_gemm's weights, in dy's type or (out_dtype torch.float32) in binary32.
+    accumulate: add to ``out`` (binary32) instead of overwriting it."""
+    _expect(dy, "dy", _HALF, (None, None))
+    rows, n = dy.shape
+    _expect(x, "x", (dy.dtype,), (rows, None))
+    k = x.shape[1]
+    _expect(counts, "counts", (torch.int32,), (None,))
+    E = counts.numel()
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate adds to an out tensor: expected one")
+        out = torch.empty((E, n, k), dtype=out_dtype or dy.dtype, device=dy.device)
+    _expect(out, "out", (dy.dtype, torch.float32) if out_dtype is None else (out_dtype,), (E, n, k))
+    if accumulate and out.dtype != torch.float32:
+        raise ValueError("accumulate: out of dtype torch.float32 expected")
+    st = status if status is not None else new_status(dy.device)
+    a = WgradArgs(_segments(counts, align, cap, rows), n, k, _TYPES[dy.dtype], _TYPES[out.dtype],
+                  int(accumulate), ptr(dy), ptr(x), ptr(out), ptr(st), num_sms_)
+    check(load().moe_grouped_wgrad(ctypes.byref(a), _ordered(stream, dy, x, counts, out, st)),
+          "moe_grouped_wgrad")
+    return out
+
+
+def swiglu(gu: torch.Tensor, row_w: torch.Tensor | None = None,
+           counts: torch.Tensor | None = None, align: int = 1, cap: int = 0,
+           out: torch.Tensor | None = None, status: torch.Tensor | None = None,
+           stream=None) -> torch.Tensor:
+    """moe_swiglu: gu bf16 / fp16 [rows][2I] (gate, then up columns) -> w silu(g) u
+    [rows][I]; row_w fp32 [rows] (default 1).  counts / align / cap: only the rows of
+    these segments (see grouped_gemm); default all rows."""
+    _expect(gu, "gu", _HALF, (None, None))
+    rows, I2 = gu.shape
+    if I2 % 2:
+        raise ValueError("gu: an even number of columns expected")
+    if row_w is not None:
+        _expect(row_w, "row_w", (torch.float32,), (rows,))
+    if out is None:
+        out = torch.empty((rows, I2 // 2), dtype=gu.dtype, device=gu.device)
+    else:
+        _expect(out, "out", (gu.dtype,), (rows, I2 // 2))
+    st = status if status is not None or counts is None else new_status(gu.device)
+    a = SwigluArgs(_segments(counts, align, cap, rows), I2 // 2, _TYPES[gu.dtype], ptr(gu), None,
+                   ptr(row_w), ptr(out), None, ptr(st))
+    check(load().moe_swiglu(ctypes.byref(a), _ordered(stream, gu, row_w, counts, out, st)),
+          "moe_swiglu")
+    return out
+
+
+def swiglu_backward(gu: torch.Tensor, dh: torch.Tensor, row_w: torch.Tensor | None = None,
+                    counts: torch.Tensor | None = None, align: int = 1, cap: int = 0,
+                    dgu: torch.Tensor | None = None, drow_w: torch.Tensor | None = None,
+                    status: torch.Tensor | None = None, stream=None):
+    """moe_swiglu_backward: dh [rows][I], the gradient of swiglu's output -> (dgu
+    [rows][2I], drow_w fp32 [rows], or None without row_w).  dgu may be gu itself."""
+    _expect(gu, "gu", _HALF, (None, None))
+    rows, I2 = gu.shape
+    if I2 % 2:
+        raise ValueError("gu: an even number of columns expected")
+    _expect(dh, "dh", (gu.dtype,), (rows, I2 // 2))
+    if row_w is not None:
+        _expect(row_w, "row_w", (torch.float32,), (rows,))
+        if drow_w is None:
+            drow_w = torch.empty(rows, dtype=torch.float32, device=gu.device)
+    if drow_w is not None:
+        _expect(drow_w, "drow_w", (torch.float32,), (rows,))
+    if dgu is None:
+        dgu = torch.empty_like(gu)
+    else:
+        _expect(dgu, "dgu", (gu.dtype,), (rows, I2))
+    st = status if status is not None or counts is None else new_status(gu.device)
+    a = SwigluArgs(_segments(counts, align, cap, rows), I2 // 2, _TYPES[gu.dtype], ptr(gu),
+                   ptr(dh), ptr(row_w), ptr(dgu), ptr(drow_w), ptr(st))
+    check(load().moe_swiglu_backward(ctypes.byref(a),
+                                     _ordered(stream, gu, dh, row_w, counts, dgu, drow_w, st)),
+          "moe_swiglu_backward")
+    return dgu, drow_w
+
+
+class AdamW:
+    """AdamW over many tensors (moe_adamw): binary32 parameters, updated in place, with
+    the moments this object holds in binary32 (state_bits 32) or in 8-bit square-law codes
+    (8, see include/moe.h), and optionally a 16-bit copy of each parameter (the model's
+    weights) refreshed by every step.
+
+    The moments live in flat buffers, each tensor's piece starting at a multiple of 256
+    values (``offsets``): ``m`` and ``v``, or ``m_code`` / ``r_code`` with ``m_scale`` /
+    ``r_scale`` per 256 values.  The parameters' and copies' addresses are taken once:
+    keep the tensors.  ``lr``, ``betas``, ``eps`` and ``weight_decay`` may be changed
+    between steps; ``steps`` counts the steps taken."""
+
+    BLOCK = 256
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay: float = 1e-2, state_bits: int = 32, copies=None):
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits: 8 or 32 expected")
+        self.params = list(params)
+        self.copies = list(copies) if copies is not None else [None] * len(self.params)
+        if not self.params or len(self.copies) != len(self.params):
+            raise ValueError("at least one parameter, and one copy (or None) for each, expected")
+        self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
+        self.state_bits, self.steps = state_bits, 0
+        self.offsets, total = [], 0
+        for p, c in zip(self.params, self.copies):
+            _expect(p, "parameter", (torch.float32,), tuple(p.shape))
+            if c is not None:
+                _expect(c, "copy", tuple(_TYPES), tuple(p.shape))
+            self.offsets.append(total)
+            total += (p.numel() + self.BLOCK - 1) // self.BLOCK * self.BLOCK
+        self.numel = total
+        dev = self.params[0].device
+        z = lambda n, dt: torch.zeros(n, dtype=dt, device=dev)  # noqa: E731
+        nb = total // self.BLOCK
+        if state_bits == 32:
+            self.m, self.v = z(total, torch.float32), z(total, torch.float32)
+        else:
+            self.m_code, self.r_code = z(total, torch.int8), z(total, torch.uint8)
+            self.m_scale, self.r_scale = z(nb, torch.float32), z(nb, torch.float32)
+        self._table = (AdamwTensor * len(self.params))()
+        for t, p, c, o in zip(self._table, self.params, self.copies, self.offsets):
+            t.n, t.p, t.copy = p.numel(), ptr(p), ptr(c)
+            if c is not None:
+                t.copy_type = _TYPES[c.dtype]
+            if state_bits == 32:
+                t.m, t.v = ptr(self.m) + 4 * o, ptr(self.v) + 4 * o
+            else:
+                t.m, t.v = ptr(self.m_code) + o, ptr(self.r_code) + o
+                t.m_scale = ptr(self.m_scale) + o // self.BLOCK * 4
+                t.r_scale = ptr(self.r_scale) + o // self.BLOCK * 4
+
+    def step(self, grads, grad_scale: torch.Tensor | None = None, stream=None) -> None:
+        """One step with one gradient (bf16, fp16 or fp32, the parameter's shape) per
+        parameter; grad_scale: fp32 device scalar that multiplies every gradient."""
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(self.params)} gradients expected, got {len(grads)}")
+        for t, p, g in zip(self._table, self.params, grads):
+            if g.dtype not in _TYPES or g.shape != p.shape:
+                raise ValueError(f"gradient: {tuple(p.shape)} of dtype bf16, fp16 or fp32 "
+                                 f"expected, got {tuple(g.shape)} {g.dtype}")
+            t.g, t.g_type = ptr(g), _TYPES[g.dtype]
+        if grad_scale is not None:
+            _expect(grad_scale, "grad_scale", (torch.float32,), tuple(grad_scale.shape))
+            if grad_scale.numel() != 1:
+                raise ValueError("grad_scale: one value expected")
+        cfg = AdamwCfg(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
+                       self.steps + 1, self.state_bits, ptr(grad_scale))
+        check(load().moe_adamw(ctypes.byref(cfg), self._table, len(self.params),
+                               _ordered(stream, *grads, grad_scale)), "moe_adamw")
+        self.steps += 1
+
+    def state(self, stream=None):
+        """The moments (m, v) in binary32, flat as ``offsets`` says: the buffers
+        themselves, or (8 bits) new tensors with the codes' values."""
+        if self.state_bits == 32:
+            return self.m, self.v
+        m, v = (torch.empty(self.numel, dtype=torch.float32, device=self.m_code.device)
+                for _ in range(2))
+        check(load().moe_adamw_decode(self.numel, ptr(self.m_code), ptr(self.m_scale),
+                                      ptr(self.r_code), ptr(self.r_scale), ptr(m), ptr(v),
+                                      _ordered(stream, m, v)), "moe_adamw_decode")
+        return m, v
+
+    def load_state(self, m: torch.Tensor, v: torch.Tensor, steps: int, stream=None) -> None:
+        """Restores what state() gave (8 bits: rounded to codes again) and the step count."""
+        for t, what in ((m, "m"), (v, "v")):
+            _expect(t, what, (torch.float32,), (self.numel,))
+        if self.state_bits == 32:
+            _ordered(stream, m, v)
+            with torch.cuda.stream(stream):
+                self.m.copy_(m)
+                self.v.copy_(v)
+        else:
+            check(load().moe_adamw_encode(self.numel, ptr(m), ptr(v), ptr(self.m_code),
+                                          ptr(self.m_scale), ptr(self.r_code),
+                                          ptr(self.r_scale), _ordered(stream, m, v)),
+                  "moe_adamw_encode")
+        self.steps = steps
 
 
 class MoELayer:

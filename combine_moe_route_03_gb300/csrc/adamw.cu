@@ -1,0 +1,448 @@
+// moe_adamw: one AdamW step over many tensors, moments in binary32 or in 8-bit
+// square-law codes with a scale per 256 values; moe_adamw_decode / _encode turn the codes
+// into binary32 moments and back.
+//
+// A warp takes a block of 256 values, 8 per lane (values 4*lane..+3 of each half, so
+// every load of the warp is contiguous); the block's largest magnitude is one warp
+// reduction, and old codes are read and new ones written in the same pass.  The tensors'
+// table travels as a kernel parameter: nothing is kept on the device between calls.
+// Bound by memory: 28 bytes a value with binary32 moments, 16-bit gradients and a 16-bit
+// copy, 16 with 8-bit moments.
+#include <cuda_fp16.h>
+#include <math.h>
+#include <string.h>
+
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBlock = 256;          // values of one 8-bit block
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr float kInvM = (float)(1.0 / 127), kInvR = (float)(1.0 / 255);
+constexpr float kSqM = 127.0f * 127.0f, kSqR = 255.0f * 255.0f;
+
+struct Entry {
+  int64_t n;
+  float *p;
+  const void *g;
+  void *copy, *m, *v;
+  float *m_scale, *r_scale;
+  int16_t g_type, copy_type;
+  int16_t aligned;  // every pointer allows 16-byte accesses of 4 values and more
+};
+
+template <int kMax>
+struct Table {
+  int n;
+  int chunk_blocks;      // blocks of one CTA's chunk
+  uint32_t chunk0[kMax + 1];
+  Entry t[kMax];
+};
+
+struct Hyper {
+  float decay, beta1, alpha1, beta2, alpha2, step, inv_bc2, eps;
+  const float *grad_scale;
+};
+
+__device__ __forceinline__ float load_g(const void *g, int type, int64_t i) {
+  if (type == MOE_TYPE_F32) return static_cast<const float *>(g)[i];
+  if (type == MOE_TYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(g)[i]);
+  return __half2float(static_cast<const __half *>(g)[i]);
+}
+__device__ __forceinline__ void store_copy(void *c, int type, int64_t i, float f) {
+  if (type == MOE_TYPE_BF16)
+    static_cast<__nv_bfloat16 *>(c)[i] = __float2bfloat16_rn(f);
+  else if (type == MOE_TYPE_F16)
+    static_cast<__half *>(c)[i] = __float2half_rn(f);
+  else
+    static_cast<float *>(c)[i] = f;
+}
+__device__ __forceinline__ void load_g4(const void *g, int type, int64_t i, float *o) {
+  if (type == MOE_TYPE_F32) {
+    const float4 q = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(g) + i));
+    o[0] = q.x, o[1] = q.y, o[2] = q.z, o[3] = q.w;
+    return;
+  }
+  const uint2 q = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(g) + i));
+  const uint32_t h[4] = {q.x & 0xffffu, q.x >> 16, q.y & 0xffffu, q.y >> 16};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    o[j] = type == MOE_TYPE_BF16 ? __uint_as_float(h[j] << 16)
+                                 : __half2float(__ushort_as_half((unsigned short)h[j]));
+}
+__device__ __forceinline__ void store_copy4(void *c, int type, int64_t i, const float *f) {
+  if (type == MOE_TYPE_F32) {
+    *reinterpret_cast<float4 *>(static_cast<float *>(c) + i) = make_float4(f[0], f[1], f[2], f[3]);
+    return;
+  }
+  uint32_t h[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    h[j] = type == MOE_TYPE_BF16 ? f32_to_bf16_bits(f[j])
+                                 : (uint32_t)__half_as_ushort(__float2half_rn(f[j]));
+  *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(c) + i) =
+      make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+// Codes: see moe_adamw in include/moe.h.
+__device__ __forceinline__ float decode_m(int c, float s) {
+  const float q = __fmul_rn((float)c, kInvM);
+  return __fmul_rn(__fmul_rn(q, fabsf(q)), s);
+}
+__device__ __forceinline__ float decode_r(int c, float s) {
+  const float q = __fmul_rn((float)c, kInvR);
+  return __fmul_rn(__fmul_rn(q, q), s);
+}
+// The whole number c with (c - 1/2)^2 <= z < (c + 1/2)^2, z = levels^2 x / s: a square
+// root of any rounding is within one of it, and the two bounds (exact in binary32) say
+// which way.
+__device__ __forceinline__ int square_code(float x, float inv, float sq, int levels) {
+  const float z = __fmul_rn(__fmul_rn(x, inv), sq);
+  float root;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(z));
+  const float c = rintf(root);
+  const float lo = c - 0.5f, hi = c + 0.5f;
+  int k = (int)c;  // NaN: 0
+  k -= (z < lo * lo && c > 0.0f) ? 1 : 0;
+  k += z >= hi * hi ? 1 : 0;
+  return min(k, levels);
+}
+__device__ __forceinline__ float block_inverse(float s) {
+  return s >= 1.17549435e-38f ? __fdiv_rn(1.0f, s) : (s != s ? s : 0.0f);
+}
+// Largest magnitude of the warp's block; a NaN wins over every number.
+__device__ __forceinline__ float block_max(const float *x) {
+  uint32_t b = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) b = max(b, __float_as_uint(x[j]) & 0x7fffffffu);
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, b));
+}
+
+// Value j (0..7) of this lane sits at this place of its block.
+__device__ __forceinline__ int place(int lane, int j) { return 128 * (j >> 2) + 4 * lane + (j & 3); }
+
+// Loads of one lane's 8 values: `n` values are left in the tensor from the block's start.
+template <class F>
+__device__ __forceinline__ void each(int lane, int64_t n, F f) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (place(lane, j) < n) f(j, place(lane, j));
+}
+
+__device__ __forceinline__ void load_f32(const float *p, bool fast, int lane, int64_t n, float *o) {
+  if (fast) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 q = __ldcs(reinterpret_cast<const float4 *>(p + place(lane, 4 * h)));
+      o[4 * h] = q.x, o[4 * h + 1] = q.y, o[4 * h + 2] = q.z, o[4 * h + 3] = q.w;
+    }
+  } else {
+    each(lane, n, [&](int j, int i) { o[j] = p[i]; });
+  }
+}
+__device__ __forceinline__ void store_f32(float *p, bool fast, int lane, int64_t n, const float *o) {
+  if (fast) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      __stcs(reinterpret_cast<float4 *>(p + place(lane, 4 * h)),
+             make_float4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]));
+  } else {
+    each(lane, n, [&](int j, int i) { p[i] = o[j]; });
+  }
+}
+__device__ __forceinline__ void load_codes(const uint8_t *p, bool fast, int lane, int64_t n, uint8_t *o) {
+  if (fast) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<uint32_t *>(o + 4 * h) =
+          __ldcs(reinterpret_cast<const uint32_t *>(p + place(lane, 4 * h)));
+  } else {
+    each(lane, n, [&](int j, int i) { o[j] = p[i]; });
+  }
+}
+__device__ __forceinline__ void store_codes(uint8_t *p, bool fast, int lane, int64_t n, const uint8_t *o) {
+  if (fast) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      __stcs(reinterpret_cast<uint32_t *>(p + place(lane, 4 * h)),
+             *reinterpret_cast<const uint32_t *>(o + 4 * h));
+  } else {
+    each(lane, n, [&](int j, int i) { p[i] = o[j]; });
+  }
+}
+struct alignas(8) Codes {
+  uint8_t c[8];
+};
+
+// New moments of a block -> codes and scales.
+__device__ __forceinline__ void encode_block(const float *m, const float *r, Codes &mc, Codes &rc,
+                                             float &ms, float &rs) {
+  ms = block_max(m);
+  rs = block_max(r);
+  const float mi = block_inverse(ms), ri = block_inverse(rs);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int c = square_code(fabsf(m[j]), mi, kSqM, 127);
+    mc.c[j] = (uint8_t)(int8_t)(m[j] < 0.0f ? -c : c);
+    const int d = square_code(r[j], ri, kSqR, 255);
+    rc.c[j] = (uint8_t)(r[j] > 0.0f ? max(d, 1) : d);
+  }
+}
+
+template <int kMax, bool k8Bit>
+__global__ void __launch_bounds__(kThreads)
+    adamw_kernel(const __grid_constant__ Table<kMax> tab, const Hyper H) {
+  // the tensor of this CTA's chunk
+  int lo = 0, hi = tab.n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tab.chunk0[mid] <= blockIdx.x)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const Entry &T = tab.t[lo];
+  const int64_t n_all = T.n;
+  const int64_t blocks = (n_all + kBlock - 1) / kBlock;
+  const int64_t first = (int64_t)(blockIdx.x - tab.chunk0[lo]) * tab.chunk_blocks;
+  const int64_t last = min(first + tab.chunk_blocks, blocks);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float gs = H.grad_scale ? *H.grad_scale : 1.0f;
+  for (int64_t b = first + warp; b < last; b += kWarps) {
+    const int64_t i0 = b * kBlock, n = n_all - i0;
+    const bool fast = T.aligned && n >= kBlock;
+    float p[8] = {}, g[8] = {}, m[8] = {}, v[8] = {}, r[8];
+    load_f32(T.p + i0, fast, lane, n, p);
+    if (fast) {
+      load_g4(T.g, T.g_type, i0 + place(lane, 0), g);
+      load_g4(T.g, T.g_type, i0 + place(lane, 4), g + 4);
+    } else {
+      each(lane, n, [&](int j, int i) { g[j] = load_g(T.g, T.g_type, i0 + i); });
+    }
+    if constexpr (k8Bit) {
+      Codes mc = {}, rc = {};
+      load_codes(static_cast<const uint8_t *>(T.m) + i0, fast, lane, n, mc.c);
+      load_codes(static_cast<const uint8_t *>(T.v) + i0, fast, lane, n, rc.c);
+      const float ms = T.m_scale[b], rs = T.r_scale[b];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        m[j] = decode_m((int8_t)mc.c[j], ms);
+        const float x = decode_r(rc.c[j], rs);
+        v[j] = __fmul_rn(x, x);
+      }
+    } else {
+      load_f32(static_cast<const float *>(T.m) + i0, fast, lane, n, m);
+      load_f32(static_cast<const float *>(T.v) + i0, fast, lane, n, v);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = H.grad_scale ? __fmul_rn(g[j], gs) : g[j];
+      m[j] = __fadd_rn(__fmul_rn(m[j], H.beta1), __fmul_rn(x, H.alpha1));
+      v[j] = __fadd_rn(__fmul_rn(v[j], H.beta2), __fmul_rn(__fmul_rn(x, x), H.alpha2));
+      r[j] = __fsqrt_rn(v[j]);
+      const float denom = fmaf(r[j], H.inv_bc2, H.eps);
+      p[j] = __fadd_rn(__fmul_rn(p[j], H.decay), -__fmul_rn(__fdiv_rn(m[j], denom), H.step));
+    }
+    store_f32(T.p + i0, fast, lane, n, p);
+    if (T.copy) {
+      if (fast) {
+        store_copy4(T.copy, T.copy_type, i0 + place(lane, 0), p);
+        store_copy4(T.copy, T.copy_type, i0 + place(lane, 4), p + 4);
+      } else {
+        each(lane, n, [&](int j, int i) { store_copy(T.copy, T.copy_type, i0 + i, p[j]); });
+      }
+    }
+    if constexpr (k8Bit) {
+      if (!fast) {  // places past the tensor's end count for nothing
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (place(lane, j) >= n) m[j] = r[j] = 0.0f;
+      }
+      Codes mc, rc;
+      float ms, rs;
+      encode_block(m, r, mc, rc, ms, rs);
+      store_codes(static_cast<uint8_t *>(T.m) + i0, fast, lane, n, mc.c);
+      store_codes(static_cast<uint8_t *>(T.v) + i0, fast, lane, n, rc.c);
+      if (lane == 0) {
+        T.m_scale[b] = ms;
+        T.r_scale[b] = rs;
+      }
+    } else {
+      store_f32(static_cast<float *>(T.m) + i0, fast, lane, n, m);
+      store_f32(static_cast<float *>(T.v) + i0, fast, lane, n, v);
+    }
+  }
+}
+
+template <bool kEncode>
+__global__ void __launch_bounds__(kThreads)
+    codes_kernel(int64_t n_all, uint8_t *m_code, float *m_scale, uint8_t *r_code, float *r_scale,
+                 float *mp, float *vp) {
+  const int64_t blocks = (n_all + kBlock - 1) / kBlock;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int64_t b = (int64_t)blockIdx.x * kWarps + warp; b < blocks; b += (int64_t)gridDim.x * kWarps) {
+    const int64_t i0 = b * kBlock, n = n_all - i0;
+    const bool fast = n >= kBlock;
+    float m[8] = {}, v[8] = {};
+    Codes mc = {}, rc = {};
+    if constexpr (kEncode) {
+      load_f32(mp + i0, fast, lane, n, m);
+      load_f32(vp + i0, fast, lane, n, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __fsqrt_rn(v[j]);
+      float ms, rs;
+      encode_block(m, v, mc, rc, ms, rs);
+      store_codes(m_code + i0, fast, lane, n, mc.c);
+      store_codes(r_code + i0, fast, lane, n, rc.c);
+      if (lane == 0) {
+        m_scale[b] = ms;
+        r_scale[b] = rs;
+      }
+    } else {
+      load_codes(m_code + i0, fast, lane, n, mc.c);
+      load_codes(r_code + i0, fast, lane, n, rc.c);
+      const float ms = m_scale[b], rs = r_scale[b];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        m[j] = decode_m((int8_t)mc.c[j], ms);
+        const float x = decode_r(rc.c[j], rs);
+        v[j] = __fmul_rn(x, x);
+      }
+      store_f32(mp + i0, fast, lane, n, m);
+      store_f32(vp + i0, fast, lane, n, v);
+    }
+  }
+}
+
+bool type_ok(int t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_F16 || t == MOE_TYPE_F32; }
+int type_size(int t) { return t == MOE_TYPE_F32 ? 4 : 2; }
+bool off(const void *p, size_t a) { return (uintptr_t)p % a != 0; }
+
+template <int kMax>
+int launch(const moe_adamw_tensor *t, int n, bool bits8, const Hyper &H, cudaStream_t st) {
+  Table<kMax> tab;
+  memset(&tab, 0, sizeof tab);
+  tab.n = n;
+  int64_t blocks = 0;
+  for (int i = 0; i < n; ++i) blocks += (t[i].n + kBlock - 1) / kBlock;
+  // 64 blocks a CTA where there is work for several rounds of CTAs, fewer (one block a
+  // warp) where the step is small
+  int chunk = 64;
+  while (chunk > kWarps && blocks / chunk < 8 * device_sm_count()) chunk >>= 1;
+  tab.chunk_blocks = chunk;
+  uint64_t chunks = 0;
+  for (int i = 0; i < n; ++i) {
+    const moe_adamw_tensor &a = t[i];
+    Entry &e = tab.t[i];
+    tab.chunk0[i] = (uint32_t)chunks;
+    chunks += (uint64_t)((a.n + kBlock - 1) / kBlock + chunk - 1) / chunk;
+    if (chunks > 0x7fffffffull) return MOE_ERR_UNSUPPORTED;
+    e.n = a.n;
+    e.p = a.p;
+    e.g = a.g;
+    e.copy = a.copy;
+    e.m = a.m;
+    e.v = a.v;
+    e.m_scale = a.m_scale;
+    e.r_scale = a.r_scale;
+    e.g_type = (int16_t)a.g_type;
+    e.copy_type = (int16_t)a.copy_type;
+    e.aligned = !(off(a.p, 16) || off(a.g, 4 * type_size(a.g_type)) ||
+                  (a.copy && off(a.copy, 4 * type_size(a.copy_type))) || off(a.m, bits8 ? 4 : 16) ||
+                  off(a.v, bits8 ? 4 : 16));
+  }
+  tab.chunk0[n] = (uint32_t)chunks;
+  if (chunks == 0) return MOE_OK;
+  if (bits8)
+    adamw_kernel<kMax, true><<<(unsigned)chunks, kThreads, 0, st>>>(tab, H);
+  else
+    adamw_kernel<kMax, false><<<(unsigned)chunks, kThreads, 0, st>>>(tab, H);
+  return check_launch();
+}
+
+int check_codes(int64_t n, const void *mc, const void *ms, const void *rc, const void *rs,
+                const void *m, const void *v) {
+  if (n < 0) return MOE_ERR_INVALID;
+  if (n > (1ll << 40)) return MOE_ERR_UNSUPPORTED;
+  if (n == 0) return MOE_OK;
+  if (!mc || !ms || !rc || !rs || !m || !v) return MOE_ERR_INVALID;
+  if (off(mc, 4) || off(rc, 4) || off(ms, 4) || off(rs, 4) || off(m, 16) || off(v, 16))
+    return MOE_ERR_INVALID;
+  return MOE_OK;
+}
+unsigned codes_grid(int64_t n) {
+  const int64_t need = ((n + kBlock - 1) / kBlock + kWarps - 1) / kWarps;
+  const int64_t most = (int64_t)device_sm_count() * 8;
+  return (unsigned)(need < most ? need : most);
+}
+
+constexpr int kSmallTable = 32, kTable = 256;
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_adamw(const moe_adamw_cfg *cfg, const moe_adamw_tensor *tensors, int n_tensors,
+                         void *stream) {
+  if (!cfg || n_tensors < 0 || (n_tensors > 0 && !tensors)) return MOE_ERR_INVALID;
+  if (cfg->state_bits != 8 && cfg->state_bits != 32) return MOE_ERR_INVALID;
+  if (cfg->step < 1 || !(cfg->beta1 >= 0 && cfg->beta1 < 1) || !(cfg->beta2 >= 0 && cfg->beta2 < 1) ||
+      !(cfg->eps >= 0) || off(cfg->grad_scale, 4))
+    return MOE_ERR_INVALID;
+  const bool bits8 = cfg->state_bits == 8;
+  for (int i = 0; i < n_tensors; ++i) {
+    const moe_adamw_tensor &t = tensors[i];
+    if (t.n < 0) return MOE_ERR_INVALID;
+    if (t.n > (1ll << 40)) return MOE_ERR_UNSUPPORTED;
+    if (!type_ok(t.g_type) || (t.copy && !type_ok(t.copy_type))) return MOE_ERR_INVALID;
+    if (t.n == 0) continue;
+    if (!t.p || !t.g || !t.m || !t.v || (bits8 && (!t.m_scale || !t.r_scale))) return MOE_ERR_INVALID;
+    if (off(t.p, 4) || off(t.g, type_size(t.g_type)) ||
+        (t.copy && off(t.copy, type_size(t.copy_type))) ||
+        (!bits8 && (off(t.m, 4) || off(t.v, 4))) || off(t.m_scale, 4) || off(t.r_scale, 4))
+      return MOE_ERR_INVALID;
+  }
+  Hyper H;
+  const double bc1 = 1.0 - pow(cfg->beta1, (double)cfg->step);
+  const double bc2 = 1.0 - pow(cfg->beta2, (double)cfg->step);
+  H.decay = (float)(1.0 - cfg->lr * cfg->weight_decay);
+  H.beta1 = (float)cfg->beta1;
+  H.alpha1 = (float)(1.0 - cfg->beta1);
+  H.beta2 = (float)cfg->beta2;
+  H.alpha2 = (float)(1.0 - cfg->beta2);
+  H.step = (float)(cfg->lr / bc1);
+  H.inv_bc2 = (float)(1.0 / sqrt(bc2));
+  H.eps = (float)cfg->eps;
+  H.grad_scale = cfg->grad_scale;
+  for (int i = 0; i < n_tensors; i += kTable) {
+    const int n = n_tensors - i < kTable ? n_tensors - i : kTable;
+    const int rc = n <= kSmallTable ? launch<kSmallTable>(tensors + i, n, bits8, H, as_stream(stream))
+                                    : launch<kTable>(tensors + i, n, bits8, H, as_stream(stream));
+    if (rc != MOE_OK) return rc;
+  }
+  return MOE_OK;
+}
+
+extern "C" int moe_adamw_decode(int64_t n, const void *m_code, const float *m_scale,
+                                const void *r_code, const float *r_scale, float *m, float *v,
+                                void *stream) {
+  const int rc = check_codes(n, m_code, m_scale, r_code, r_scale, m, v);
+  if (rc != MOE_OK || n == 0) return rc;
+  codes_kernel<false><<<codes_grid(n), kThreads, 0, as_stream(stream)>>>(
+      n, static_cast<uint8_t *>(const_cast<void *>(m_code)), const_cast<float *>(m_scale),
+      static_cast<uint8_t *>(const_cast<void *>(r_code)), const_cast<float *>(r_scale), m, v);
+  return check_launch();
+}
+
+extern "C" int moe_adamw_encode(int64_t n, const float *m, const float *v, void *m_code,
+                                float *m_scale, void *r_code, float *r_scale, void *stream) {
+  const int rc = check_codes(n, m_code, m_scale, r_code, r_scale, m, v);
+  if (rc != MOE_OK || n == 0) return rc;
+  codes_kernel<true><<<codes_grid(n), kThreads, 0, as_stream(stream)>>>(
+      n, static_cast<uint8_t *>(m_code), m_scale, static_cast<uint8_t *>(r_code), r_scale,
+      const_cast<float *>(m), const_cast<float *>(v));
+  return check_launch();
+}

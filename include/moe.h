@@ -448,6 +448,177 @@ int moe_combine(const moe_combine_cfg *cfg, const void *Y, const int32_t *row_of
                 const float *topk_w, const void *shared, void *out, int32_t *status,
                 void *stream);
 
+/* ------------------------------------------------- experts in 16-bit storage */
+/*
+ * Operators for experts kept in bf16 or fp16 and for their training: the products of
+ * an expert FFN without quantisation, their gradients, the gated activation between
+ * them and its gradient, and an AdamW step.  (The pages cover inference only; these
+ * entry points have no counterpart there.)  They read the same row layouts that
+ * moe_dispatch writes (its BF16 format), so with the row weight folded into the
+ * activation the layer's gradients need no kernel of their own for the permutation:
+ * the gradient of the combine with respect to the rows is moe_dispatch of the output
+ * gradient, and the gradient of the dispatch is moe_combine with unit weights.
+ *
+ * Element types of the 16-bit tensors and of binary32 outputs.
+ */
+#define MOE_TYPE_BF16 0
+#define MOE_TYPE_F16 1
+#define MOE_TYPE_F32 2
+
+/*
+ * Ragged segments of a row buffer of `rows` rows, one segment per expert:
+ *   cap == 0: expert e's segment starts at sum_{q<e} roundup(counts[q], align) (align
+ *     128: moe_dispatch's CONTIG layout; 1: rows packed without padding);
+ *   cap > 0: it starts at e*cap and holds min(counts[e], cap) rows (the MASKED layout).
+ * counts is device int32 [E], so the host never sees the routing.  Rows outside the
+ * segments (padding) are neither read into a result nor written; they may hold anything.
+ * What the device finds wrong is bounded, not followed: a negative count counts as 0 and
+ * sets MOE_STATUS_BAD_INDEX; a segment that passes `rows` is cut there, and a count
+ * above cap cut to it, and both set MOE_STATUS_CAPACITY.
+ * Limits: 1 <= E <= 1024, align >= 1, cap >= 0, 0 <= rows <= 2^31 - 1 - 1024.
+ */
+typedef struct moe_segments {
+  const int32_t *counts;
+  int E;
+  int align;
+  int cap;
+  int64_t rows;
+} moe_segments;
+
+/*
+ * Grouped product over ragged segments, 16-bit operands of one type, binary32 sums:
+ *   trans == 0: out[r][j] = sum_i x[r][i] * w[e][j][i], x [rows][k], out [rows][n] (an
+ *     expert's forward product);
+ *   trans == 1: out[r][i] = sum_j x[r][j] * w[e][j][i], x [rows][n], out [rows][k] (the
+ *     gradient of that product with respect to its input, or the forward product of
+ *     weights stored [k][n]);
+ * for every row r of expert e's segment, w [E][n][k]; one rounding to the 16-bit type
+ * at the end.  num_sms: CTAs of the persistent grid (0: every SM).
+ * Errors, before any launch: MOE_ERR_INVALID for a null pointer, a bad type or size, or
+ * x, w or out not 16-byte aligned; MOE_ERR_UNSUPPORTED for n or k not a multiple of 8
+ * or sizes outside the limits above.  rows == 0 enqueues nothing.
+ */
+typedef struct moe_ggemm_args {
+  moe_segments seg;
+  int n, k;
+  int trans;
+  int type;
+  const void *x, *w;
+  void *out;
+  int32_t *status;
+  int num_sms;
+} moe_ggemm_args;
+
+int moe_grouped_gemm(const moe_ggemm_args *args, void *stream);
+
+/*
+ * Weight gradient of the grouped product: dw[e][j][i] = sum over the rows r of expert
+ * e's segment of dy[r][j] * x[r][i], dy [rows][n], x [rows][k], out [E][n][k].
+ *   out_type: `type` (one rounding at the end) or MOE_TYPE_F32.  accumulate != 0 (with
+ *   MOE_TYPE_F32): out += dw (gradients over several micro-batches); experts without
+ *   rows then keep their values, and otherwise get zeros.
+ *   With MOE_TYPE_F32 partial sums of at most 512 rows are joined by binary32 additions
+ *   (the tensor core's own accumulation truncates, which would show over long segments).
+ *   The order of the additions is fixed: the same inputs give the same bits.
+ * Limits and errors as moe_grouped_gemm; a bad out_type, or accumulate without
+ * MOE_TYPE_F32: MOE_ERR_INVALID.
+ */
+typedef struct moe_wgrad_args {
+  moe_segments seg;
+  int n, k;
+  int type;
+  int out_type;
+  int accumulate;
+  const void *dy, *x;
+  void *out;
+  int32_t *status;
+  int num_sms;
+} moe_wgrad_args;
+
+int moe_grouped_wgrad(const moe_wgrad_args *args, void *stream);
+
+/*
+ * Gated activation and its gradient, over the rows of the segments (seg.counts NULL: all
+ * seg.rows rows, E, align and cap unused).  gu [rows][2I]: gate g in columns [0, I), up
+ * u in [I, 2I); a = g sigmoid(g); row_w float [rows] (nullable: 1) the row's weight w.
+ *   moe_swiglu:          out [rows][I]  = w a u
+ *   moe_swiglu_backward: out [rows][2I] = (w dh u sigmoid(g) (1 + g sigmoid(-g)), w dh a)
+ *     and, with drow_w non-NULL, drow_w[r] = sum_j dh a u (the gradient of w[r]),
+ *     for dh [rows][I] the gradient of the activation.
+ * Computed in binary32, rounded once.  drow_w is summed in a fixed order.  The
+ * backward's out may be gu itself.  I >= 1; any alignment of the element type (16-byte aligned tensors with
+ * I % 8 == 0 take the fast path).  Errors: MOE_ERR_INVALID for a null pointer, a bad
+ * type or size; MOE_ERR_UNSUPPORTED outside the limits of the segments, or I > 2^24.
+ */
+typedef struct moe_swiglu_args {
+  moe_segments seg;
+  int I;
+  int type;
+  const void *gu;
+  const void *dh;      /* backward only */
+  const float *row_w;
+  void *out;
+  float *drow_w;       /* backward only, nullable */
+  int32_t *status;
+} moe_swiglu_args;
+
+int moe_swiglu(const moe_swiglu_args *args, void *stream);
+int moe_swiglu_backward(const moe_swiglu_args *args, void *stream);
+
+/*
+ * One AdamW step over many tensors, in as few launches as their table fits (256 tensors
+ * each).  With g the gradient (times *grad_scale, a device float, where given):
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 -
+ *   beta2^step) + eps), and copy = p rounded to its type, where a copy is kept
+ * in binary32, each sum and product of m and v rounded by itself (no fused
+ * multiply-add), so the moments are reproducible bit for bit.  step counts from 1.
+ * state_bits 32: m, v float [n].  state_bits 8: square-law codes of the blocks of 256
+ * consecutive values, with a binary32 scale per block:
+ *   m = s q |q|, q = code / 127 (int8), s the block's largest |m|;
+ *   sqrt(v) = s q^2, q = code / 255 (uint8), s the block's largest sqrt(v);
+ *   the code c of a magnitude x is the whole number with (c - 1/2)^2 <= L^2 x / s <
+ *   (c + 1/2)^2 (L = 127 or 255), at least 1 for sqrt(v) > 0 (a second moment that
+ *   vanished would divide the step by eps).  The square law keeps the relative step at
+ *   2 / L for the largest values and reaches down to 1e-5 of them.  A block whose
+ *   largest value is below 2^-126 is held as zeros; a NaN in a block makes its scale NaN.
+ *   m_code int8 [n], r_code uint8 [n], m_scale and r_scale float [ceil(n / 256)].
+ * The update of p uses the new moments before they are rounded to codes.
+ * `tensors` is a host array.  A tensor's pointers need the alignment of their element;
+ * 16-byte aligned ones take the fast path.  Errors, before any launch: MOE_ERR_INVALID
+ * for a null pointer, n < 0, a bad type, state_bits, step < 1, betas outside [0, 1), eps
+ * < 0 or a pointer off its element's alignment; MOE_ERR_UNSUPPORTED for n > 2^40.
+ */
+typedef struct moe_adamw_cfg {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+  int state_bits;
+  const float *grad_scale;
+} moe_adamw_cfg;
+
+typedef struct moe_adamw_tensor {
+  int64_t n;
+  float *p;
+  const void *g;
+  void *copy; /* nullable */
+  void *m;    /* float or int8 codes */
+  void *v;    /* float or uint8 codes of sqrt(v) */
+  float *m_scale, *r_scale; /* 8 bits only */
+  int g_type, copy_type;    /* MOE_TYPE_* */
+} moe_adamw_tensor;
+
+int moe_adamw(const moe_adamw_cfg *cfg, const moe_adamw_tensor *tensors, int n_tensors,
+              void *stream);
+
+/* 8-bit moments of n consecutive values (whole blocks first, then one partial block)
+   to binary32 and back: what a checkpoint stores, and what restores it.  m_code, r_code
+   4-byte aligned, m and v 16-byte aligned.  Errors: n < 0, a null pointer or a bad
+   alignment: MOE_ERR_INVALID; n > 2^40: MOE_ERR_UNSUPPORTED. */
+int moe_adamw_decode(int64_t n, const void *m_code, const float *m_scale, const void *r_code,
+                     const float *r_scale, float *m, float *v, void *stream);
+int moe_adamw_encode(int64_t n, const float *m, const float *v, void *m_code, float *m_scale,
+                     void *r_code, float *r_scale, void *stream);
+
 /* ------------------------------------------------------------------ status */
 /* Copies the device status word to *host_status (synchronous). */
 int moe_read_status(const int32_t *status, int32_t *host_status);
