@@ -212,6 +212,22 @@ def ptr(t, host: bool = False) -> int | None:
     return int(t)
 
 
+def ptrs(*tensors) -> list:
+    """ptr of each device tensor (None stays None), the current device looked up once."""
+    out, dev = [], -1
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if dev < 0 and t.is_cuda:
+            dev = torch.cuda.current_device()
+        if t.is_cuda and t.get_device() == dev and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            out.append(ptr(t))  # raises
+    return out
+
+
 def stream_ptr(stream=None) -> int:
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream

@@ -14,7 +14,7 @@ from . import _lib
 from ._lib import (FMT_BF16, FMT_FP8, FMT_FP8_F32, GEMM_DOWN, GEMM_GATEUP_SWIGLU, SCALE_F32,
                    SCALE_UE8M0, AdamwCfg, AdamwTensor, CombineCfg, DispatchCfg, EplbCfg,
                    FusedCombine, GemmArgs, GgemmArgs, Layer, RouteCfg, Segments, SwigluArgs,
-                   WgradArgs, check, load, ptr, stream_ptr)
+                   WgradArgs, check, load, ptr, ptrs, stream_ptr)
 from .configs import MASKED, MoEConfig
 
 __all__ = ["route", "eplb_build_map", "eplb_plan", "check_eplb_map", "EplbRecorder", "dispatch", "dispatch_sizes", "pack_weight_scales",
@@ -376,11 +376,23 @@ _TYPES = {torch.bfloat16: _lib.TYPE_BF16, torch.float16: _lib.TYPE_F16,
 _HALF = (torch.bfloat16, torch.float16)
 
 
-def _segments(counts: torch.Tensor | None, align: int, cap: int, rows: int) -> Segments:
-    if counts is None:
-        return Segments(None, 0, 1, 0, rows)
-    _expect(counts, "counts", (torch.int32,), (None,))
-    return Segments(ptr(counts), counts.numel(), align, cap, rows)
+def _is(t, what: str, dtype: torch.dtype, shape: tuple) -> None:
+    """_expect of one dtype and a whole shape; the usual case costs two comparisons."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape):
+        _expect(t, what, (dtype,), shape)
+
+
+def _on(stream, *tensors) -> int:
+    """_ordered for calls that may take another stream: its inputs and outputs too are
+    kept from reuse until that stream is done with them."""
+    if stream is None:      # the current device's current stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return _ordered(stream, *tensors)
+
+
+def _segments(counts: torch.Tensor | None, address: int | None, align: int, cap: int,
+              rows: int) -> Segments:
+    return Segments(address, 0 if counts is None else counts.shape[0], align, cap, rows)
 
 
 def grouped_gemm(x: torch.Tensor, w: torch.Tensor, counts: torch.Tensor, trans: bool = False,
@@ -391,21 +403,22 @@ def grouped_gemm(x: torch.Tensor, w: torch.Tensor, counts: torch.Tensor, trans: 
     x [rows][k] -> out [rows][n], or with ``trans`` x [rows][n] -> out [rows][k].
     counts int32 [E]: rows of each expert; align / cap: where the segments start
     (align 128: a contiguous dispatch, 1: packed rows; cap: a masked dispatch).  Rows
-    outside the segments are not written."""
+    outside the segments are not written.  status: int32 word for what the device finds
+    wrong with the counts (new_status; without one it is not reported)."""
     _expect(w, "w", _HALF, (None, None, None))
     E, n, k = w.shape
     red, cols = (n, k) if trans else (k, n)
-    _expect(x, "x", (w.dtype,), (None, red))
-    _expect(counts, "counts", (torch.int32,), (E,))
     rows = x.shape[0]
+    _is(x, "x", w.dtype, (rows, red))
+    _is(counts, "counts", torch.int32, (E,))
     if out is None:
         out = torch.empty((rows, cols), dtype=w.dtype, device=x.device)
     else:
-        _expect(out, "out", (w.dtype,), (rows, cols))
-    st = status if status is not None else new_status(x.device)
-    a = GgemmArgs(_segments(counts, align, cap, rows), n, k, int(trans), _TYPES[w.dtype], ptr(x),
-                  ptr(w), ptr(out), ptr(st), num_sms_)
-    check(load().moe_grouped_gemm(ctypes.byref(a), _ordered(stream, x, w, counts, out, st)),
+        _is(out, "out", w.dtype, (rows, cols))
+    pc, px, pw, po, ps = ptrs(counts, x, w, out, status)
+    a = GgemmArgs(_segments(counts, pc, align, cap, rows), n, k, int(trans), _TYPES[w.dtype], px,
+                  pw, po, ps, num_sms_)
+    check(load().moe_grouped_gemm(ctypes.byref(a), _on(stream, x, w, counts, out, status)),
           "moe_grouped_gemm")
     return out
 
@@ -423,7 +436,7 @@ def grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, counts: torch.Tensor, align
     _expect(x, "x", (dy.dtype,), (rows, None))
     k = x.shape[1]
     _expect(counts, "counts", (torch.int32,), (None,))
-    E = counts.numel()
+    E = counts.shape[0]
     if out is None:
         if accumulate:
             raise ValueError("accumulate adds to an out tensor: expected one")
@@ -431,10 +444,10 @@ def grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, counts: torch.Tensor, align
     _expect(out, "out", (dy.dtype, torch.float32) if out_dtype is None else (out_dtype,), (E, n, k))
     if accumulate and out.dtype != torch.float32:
         raise ValueError("accumulate: out of dtype torch.float32 expected")
-    st = status if status is not None else new_status(dy.device)
-    a = WgradArgs(_segments(counts, align, cap, rows), n, k, _TYPES[dy.dtype], _TYPES[out.dtype],
-                  int(accumulate), ptr(dy), ptr(x), ptr(out), ptr(st), num_sms_)
-    check(load().moe_grouped_wgrad(ctypes.byref(a), _ordered(stream, dy, x, counts, out, st)),
+    pc, pd, px, po, ps = ptrs(counts, dy, x, out, status)
+    a = WgradArgs(_segments(counts, pc, align, cap, rows), n, k, _TYPES[dy.dtype],
+                  _TYPES[out.dtype], int(accumulate), pd, px, po, ps, num_sms_)
+    check(load().moe_grouped_wgrad(ctypes.byref(a), _on(stream, dy, x, counts, out, status)),
           "moe_grouped_wgrad")
     return out
 
@@ -444,22 +457,24 @@ def swiglu(gu: torch.Tensor, row_w: torch.Tensor | None = None,
            out: torch.Tensor | None = None, status: torch.Tensor | None = None,
            stream=None) -> torch.Tensor:
     """moe_swiglu: gu bf16 / fp16 [rows][2I] (gate, then up columns) -> w silu(g) u
-    [rows][I]; row_w fp32 [rows] (default 1).  counts / align / cap: only the rows of
-    these segments (see grouped_gemm); default all rows."""
+    [rows][I]; row_w fp32 [rows] (default 1).  counts / align / cap / status: only the
+    rows of these segments (see grouped_gemm); default all rows."""
     _expect(gu, "gu", _HALF, (None, None))
     rows, I2 = gu.shape
     if I2 % 2:
         raise ValueError("gu: an even number of columns expected")
     if row_w is not None:
-        _expect(row_w, "row_w", (torch.float32,), (rows,))
+        _is(row_w, "row_w", torch.float32, (rows,))
+    if counts is not None:
+        _expect(counts, "counts", (torch.int32,), (None,))
     if out is None:
         out = torch.empty((rows, I2 // 2), dtype=gu.dtype, device=gu.device)
     else:
-        _expect(out, "out", (gu.dtype,), (rows, I2 // 2))
-    st = status if status is not None or counts is None else new_status(gu.device)
-    a = SwigluArgs(_segments(counts, align, cap, rows), I2 // 2, _TYPES[gu.dtype], ptr(gu), None,
-                   ptr(row_w), ptr(out), None, ptr(st))
-    check(load().moe_swiglu(ctypes.byref(a), _ordered(stream, gu, row_w, counts, out, st)),
+        _is(out, "out", gu.dtype, (rows, I2 // 2))
+    pc, pg, pw, po, ps = ptrs(counts, gu, row_w, out, status)
+    a = SwigluArgs(_segments(counts, pc, align, cap, rows), I2 // 2, _TYPES[gu.dtype], pg, None,
+                   pw, po, None, ps)
+    check(load().moe_swiglu(ctypes.byref(a), _on(stream, gu, row_w, counts, out, status)),
           "moe_swiglu")
     return out
 
@@ -474,22 +489,24 @@ def swiglu_backward(gu: torch.Tensor, dh: torch.Tensor, row_w: torch.Tensor | No
     rows, I2 = gu.shape
     if I2 % 2:
         raise ValueError("gu: an even number of columns expected")
-    _expect(dh, "dh", (gu.dtype,), (rows, I2 // 2))
+    _is(dh, "dh", gu.dtype, (rows, I2 // 2))
     if row_w is not None:
-        _expect(row_w, "row_w", (torch.float32,), (rows,))
+        _is(row_w, "row_w", torch.float32, (rows,))
         if drow_w is None:
             drow_w = torch.empty(rows, dtype=torch.float32, device=gu.device)
     if drow_w is not None:
-        _expect(drow_w, "drow_w", (torch.float32,), (rows,))
+        _is(drow_w, "drow_w", torch.float32, (rows,))
+    if counts is not None:
+        _expect(counts, "counts", (torch.int32,), (None,))
     if dgu is None:
         dgu = torch.empty_like(gu)
     else:
-        _expect(dgu, "dgu", (gu.dtype,), (rows, I2))
-    st = status if status is not None or counts is None else new_status(gu.device)
-    a = SwigluArgs(_segments(counts, align, cap, rows), I2 // 2, _TYPES[gu.dtype], ptr(gu),
-                   ptr(dh), ptr(row_w), ptr(dgu), ptr(drow_w), ptr(st))
+        _is(dgu, "dgu", gu.dtype, (rows, I2))
+    pc, pg, pd, pw, po, pr, ps = ptrs(counts, gu, dh, row_w, dgu, drow_w, status)
+    a = SwigluArgs(_segments(counts, pc, align, cap, rows), I2 // 2, _TYPES[gu.dtype], pg, pd, pw,
+                   po, pr, ps)
     check(load().moe_swiglu_backward(ctypes.byref(a),
-                                     _ordered(stream, gu, dh, row_w, counts, dgu, drow_w, st)),
+                                     _on(stream, gu, dh, row_w, counts, dgu, drow_w, status)),
           "moe_swiglu_backward")
     return dgu, drow_w
 
@@ -551,11 +568,12 @@ class AdamW:
         parameter; grad_scale: fp32 device scalar that multiplies every gradient."""
         if len(grads) != len(self.params):
             raise ValueError(f"{len(self.params)} gradients expected, got {len(grads)}")
-        for t, p, g in zip(self._table, self.params, grads):
-            if g.dtype not in _TYPES or g.shape != p.shape:
+        for t, p, g, a in zip(self._table, self.params, grads, ptrs(*grads)):
+            kind = _TYPES.get(g.dtype)
+            if kind is None or g.shape != p.shape:
                 raise ValueError(f"gradient: {tuple(p.shape)} of dtype bf16, fp16 or fp32 "
                                  f"expected, got {tuple(g.shape)} {g.dtype}")
-            t.g, t.g_type = ptr(g), _TYPES[g.dtype]
+            t.g, t.g_type = a, kind
         if grad_scale is not None:
             _expect(grad_scale, "grad_scale", (torch.float32,), tuple(grad_scale.shape))
             if grad_scale.numel() != 1:
@@ -563,7 +581,7 @@ class AdamW:
         cfg = AdamwCfg(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
                        self.steps + 1, self.state_bits, ptr(grad_scale))
         check(load().moe_adamw(ctypes.byref(cfg), self._table, len(self.params),
-                               _ordered(stream, *grads, grad_scale)), "moe_adamw")
+                               _on(stream, *grads, grad_scale)), "moe_adamw")
         self.steps += 1
 
     def state(self, stream=None):
@@ -575,7 +593,7 @@ class AdamW:
                 for _ in range(2))
         check(load().moe_adamw_decode(self.numel, ptr(self.m_code), ptr(self.m_scale),
                                       ptr(self.r_code), ptr(self.r_scale), ptr(m), ptr(v),
-                                      _ordered(stream, m, v)), "moe_adamw_decode")
+                                      _on(stream, m, v)), "moe_adamw_decode")
         return m, v
 
     def load_state(self, m: torch.Tensor, v: torch.Tensor, steps: int, stream=None) -> None:

@@ -39,11 +39,14 @@ namespace {
 
 constexpr int kFwd = 0, kTrans = 1, kGrad = 2;
 constexpr int kThreads = 384, kEpiWarps = 8;
-constexpr int BP = 256, BQ = 256, BT = 64;  // tile of a CTA pair, depth of a stage
-constexpr int kStages = 6, kUnitQ = 8;
-constexpr uint32_t kPBytes = 128 * BT * 2, kQBytes = 128 * BT * 2;  // a CTA's halves
-constexpr uint32_t kBoxRows = 32;                                   // rows of one Q box
+constexpr int BP = 256, BQ = 256, BT = 64;  // tile of a CTA pair, depth of a block of t
+constexpr int kWide = 2 * BQ;               // q's of a wide unit
+constexpr int kSlots = 12, kUnitQ = 8;
+constexpr uint32_t kSlotBytes = 128 * BT * 2;  // a CTA's half of a P or Q tile
+constexpr uint32_t kBoxRows = 32;              // rows of one Q box
+constexpr uint32_t kStageBytes = 32 * 64;      // an epilogue warp's 32 x 32 16-bit block
 constexpr int kSumBlocks = 8;  // blocks of one partial sum (binary32 output): 512 rows
+constexpr int kWideRows = 1024;  // rows from which the gradient takes wide units
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -51,8 +54,8 @@ struct Unit {
   int z;      // expert
   int p0;     // first p of the pair's tile
   int q0;     // first q: a row of the buffer (forward, trans), a column of dy (gradient)
-  int nq;     // q's that exist, at most 256
-  int n;      // N of the MMAs
+  int nq;     // q's that exist, at most 512
+  int n[2];   // N of the MMAs of each accumulator (n[1] 0: one accumulator)
   int t0;     // first t: 0, or the segment's first row (gradient)
   int blocks; // 64-deep blocks of t
   int rem;    // t's of the last block, 1..64
@@ -60,8 +63,20 @@ struct Unit {
   int end;
 };
 
+// A place in the ring of operand slots.
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == kSlots) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 struct Shared {
-  uint64_t full[kStages], empty[kStages], tail[kStages];
+  uint64_t full[kSlots], empty[kSlots], tail[kSlots];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t unit_full[kUnitQ], unit_empty[kUnitQ];
   Unit unit[kUnitQ];
@@ -70,7 +85,8 @@ struct Shared {
   long long part[33];
   SegTable table;
 };
-constexpr uint32_t kOffShared = kStages * (kPBytes + kQBytes);
+constexpr uint32_t kOffStage = kSlots * kSlotBytes;
+constexpr uint32_t kOffShared = kOffStage + kEpiWarps * kStageBytes;
 constexpr uint32_t kSmemBytes = kOffShared + sizeof(Shared) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory");
 
@@ -119,6 +135,53 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t *r) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+// 32 columns of 16 TMEM lanes, as 16 x 8 blocks: r[4i], r[4i+1] hold lane t/4, columns
+// 8i + 2(t%4) and +1 of thread t, r[4i+2], r[4i+3] lane t/4 + 8.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// Four 8x8 blocks of 16-bit values, each stored transposed; lane 8m + j gives the address
+// of row j of block m.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b,
+                                                  uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+// Arrive on an mbarrier of either CTA of the pair where only the count matters (operands
+// land by TMA, accumulators are read by tcgen05.ld): no cluster-wide release, which would
+// first wait for the warp's global stores.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+// One lane of a converged warp, chosen so that the compiler knows it is one: the
+// descriptors of MMAs and copies sit in uniform registers, and behind `lane == 0` each
+// would be issued through a loop over the lanes (80 cycles an MMA instead of 45).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void tma_store_3d(const void *map, uint32_t src, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+      "r"(src), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// The thread's bulk stores have read their shared memory / are complete.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -132,9 +195,10 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t base, int step) {
 }
 
 // ------------------------------------------------------------------- schedule
-// Rows of a segment's row tiles: the fewest tiles of at most 256, evened out.
+// Rows of a segment's row tiles: one tile of up to 256 (one accumulator, the other one
+// takes the next unit's MMAs meanwhile), else the fewest of up to 512 (both), evened out.
 __device__ __forceinline__ int tile_rows(int count) {
-  const int tiles = (count + BQ - 1) / BQ;
+  const int tiles = (count + kWide - 1) / kWide;
   return ((count + tiles - 1) / tiles + 31) / 32 * 32;
 }
 __device__ __forceinline__ int row_tiles(int count) {
@@ -142,35 +206,47 @@ __device__ __forceinline__ int row_tiles(int count) {
   const int rows = tile_rows(count);
   return (count + rows - 1) / rows;
 }
+// N of each accumulator for nq q's, in multiples of `step`.
+__device__ __forceinline__ void split_n(Unit &U, int step) {
+  if (U.nq <= BQ) {
+    U.n[0] = (U.nq + step - 1) / step * step;
+    U.n[1] = 0;
+  } else {
+    U.n[0] = ((U.nq + 1) / 2 + step - 1) / step * step;
+    U.n[1] = (U.nq - U.n[0] + step - 1) / step * step;
+  }
+}
+// The gradient's q's of a unit: 512 where the segment is long enough for the MMAs to
+// hide the stores of two accumulators, and sums are not kept in registers.
+template <bool kF32>
+__device__ __forceinline__ int grad_q(int nq, int count) {
+  return !kF32 && nq > BQ && count >= kWideRows ? kWide : BQ;
+}
 
 // Unit u: the segments in order, within one the p tiles, within one the row tiles (or, for
 // the gradient, the q tiles), so units that share a weight tile run side by side.
-template <int kMode>
-__device__ __forceinline__ Unit get_unit(const GroupedParams &P, const SegTable &T, int64_t u,
+template <int kMode, bool kF32>
+__device__ __forceinline__ Unit get_unit(const GroupedParams &P, const SegTable &T, int u,
                                          int p_tiles) {
   Unit U = {};
+  const int e = find_segment(T, P.seg.E, u / p_tiles);
+  const int tiles = T.before[e + 1] - T.before[e];  // q tiles of the segment
+  const int local = u - T.before[e] * p_tiles, qt = local % tiles, count = T.count[e];
+  U.z = e;
+  U.p0 = local / tiles * BP;
   if constexpr (kMode == kGrad) {
-    const int q_tiles = (P.nq + BQ - 1) / BQ, per = p_tiles * q_tiles;
-    const int e = find_segment(T, P.seg.E, (int)(u / per));
-    const int local = (int)(u % per);
-    U.z = e;
-    U.p0 = local / q_tiles * BP;
-    U.q0 = local % q_tiles * BQ;
-    U.nq = min(BQ, P.nq - U.q0);
-    U.n = U.nq > 128 ? 256 : 128;  // whole 64-wide column blocks in each CTA
+    const int q = grad_q<kF32>(P.nq, count);
+    U.q0 = qt * q;
+    U.nq = min(q, P.nq - U.q0);
+    split_n(U, 128);  // whole 64-wide column blocks in each CTA
     U.t0 = T.start[e];
-    U.blocks = (T.count[e] + BT - 1) / BT;
-    U.rem = T.count[e] - (U.blocks - 1) * BT;
+    U.blocks = (count + BT - 1) / BT;
+    U.rem = count - (U.blocks - 1) * BT;
   } else {
-    const int e = find_segment(T, P.seg.E, (int)(u / p_tiles));
-    const int tiles = T.before[e + 1] - T.before[e], rows = tile_rows(T.count[e]);
-    const int64_t local = u - (int64_t)T.before[e] * p_tiles;
-    const int qt = (int)(local % tiles);
-    U.z = e;
-    U.p0 = (int)(local / tiles) * BP;
+    const int rows = tile_rows(count);
     U.q0 = T.start[e] + qt * rows;
-    U.nq = min(rows, T.count[e] - qt * rows);
-    U.n = (U.nq + 31) / 32 * 32;
+    U.nq = min(rows, count - qt * rows);
+    split_n(U, 32);
     U.blocks = (P.nt + BT - 1) / BT;
     U.rem = P.nt - (U.blocks - 1) * BT;
     U.once = tiles == 1;
@@ -180,39 +256,45 @@ __device__ __forceinline__ Unit get_unit(const GroupedParams &P, const SegTable 
 
 // ------------------------------------------------------------------- epilogue
 template <class O>
-__device__ __forceinline__ uint32_t pack2(float a, float b);
-template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
-  return f32_to_bf16_bits(a) | (f32_to_bf16_bits(b) << 16);
-}
-template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
-  return (uint32_t)__half_as_ushort(__float2half_rn(a)) |
-         ((uint32_t)__half_as_ushort(__float2half_rn(b)) << 16);
+__device__ __forceinline__ uint32_t pack2(uint32_t lo, uint32_t hi) {
+  uint32_t r;
+  if constexpr (sizeof(O) == 2 && !__is_same(O, __half))
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
+  return r;
 }
 
-// 32 columns (q0 + 0..31) of this warp's 32 lanes (p0 + lane) to the rows of a 16-bit
-// output.  Neighbouring lanes swap one of each two columns, so that a lane holds two
-// consecutive p of one row: 4-byte stores, 64 contiguous bytes a row.  np is even and p0 a
-// multiple of 32, so a pair is inside or outside as one.
+// 32 accumulator columns (q) of this warp's 32 lanes (p) -> 16-bit rows [q][p] of 64 bytes
+// in the warp's staging block, 16-byte pieces swizzled by row (the 64-byte TMA swizzle:
+// neither these writes nor the copies out conflict on banks).
+__device__ __forceinline__ uint32_t stage_offset(int q, int piece) {
+  return 64 * q + 16 * (piece ^ ((q >> 1) & 3));
+}
 template <class O>
-__device__ __forceinline__ void store_columns(const uint32_t *v, uint16_t *out, int64_t pitch,
-                                              int p, int np, int nq, int lane) {
-  const int odd = lane & 1;
-  uint16_t *o = out + (p - odd) + odd * pitch;
+__device__ __forceinline__ void stage_block(uint32_t taddr, bool zero, uint32_t stage, int lane) {
+  const int m = lane >> 3, j = lane & 7;
 #pragma unroll
-  for (int j = 0; j < 32; j += 2) {
-    const float a = __uint_as_float(v[j]), b = __uint_as_float(v[j + 1]);
-    const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-    const uint32_t w = odd ? pack2<O>(got, b) : pack2<O>(a, got);
-    if (p < np && j + odd < nq) *reinterpret_cast<uint32_t *>(o + (int64_t)j * pitch) = w;
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[16];
+    tmem_ld_16x256b_x4(taddr + ((uint32_t)(16 * h) << 16), v);
+    tc_wait_ld();
+    if (zero) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i += 2)
+      stmatrix_x4_trans(stage + stage_offset(8 * (i + (m >> 1)) + j, 2 * h + (m & 1)),
+                        pack2<O>(v[4 * i], v[4 * i + 1]), pack2<O>(v[4 * i + 2], v[4 * i + 3]),
+                        pack2<O>(v[4 * i + 4], v[4 * i + 5]), pack2<O>(v[4 * i + 6], v[4 * i + 7]));
   }
 }
 
 template <int kMode, class O>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
-                   const GroupedParams P) {
+                   const __grid_constant__ CUtensorMap tmO, const GroupedParams P) {
   constexpr bool kF32 = sizeof(O) == 4;
   constexpr bool kPMn = kMode != kFwd, kQMn = kMode == kGrad;
   extern __shared__ uint8_t smem_raw[];
@@ -220,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Shared &S = *reinterpret_cast<Shared *>(smem + kOffShared);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t s_p = smem_u32(smem), s_q = s_p + kStages * kPBytes;
+  const uint32_t s_slots = smem_u32(smem);
   const uint32_t bar_full = smem_u32(S.full), bar_empty = smem_u32(S.empty);
   const uint32_t bar_tail = smem_u32(S.tail);
   const uint32_t bar_acc_full = smem_u32(S.acc_full), bar_acc_empty = smem_u32(S.acc_empty);
@@ -230,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rank = (int)cluster_ctarank();
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kSlots; ++s) {
       mbar_init(bar_full + 8 * s, kMode == kGrad ? 2 : 1);  // gradient: each CTA arrives
       mbar_init(bar_empty + 8 * s, 1);
       mbar_init(bar_tail + 8 * s, 1);
@@ -248,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     tma_prefetch_desc(&tmP);
     tma_prefetch_desc(&tmQ);
+    if (!kF32) tma_prefetch_desc(&tmO);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(&S.tmem), kTmemCols);
@@ -256,7 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   build_segments(
       P.seg, S.table, S.part,
       [&](int n) {
-        if constexpr (kMode == kGrad) return P.accumulate && n == 0 ? 0 : 1;
+        if constexpr (kMode == kGrad) {
+          const int q = grad_q<kF32>(P.nq, n);
+          return P.accumulate && n == 0 ? 0 : (P.nq + q - 1) / q;
+        }
         return row_tiles(n);
       },
       cluster_id_x() == 0 && rank == 0);
@@ -266,8 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = S.tmem;
   const int p_tiles = (P.np + BP - 1) / BP;
-  const int64_t units = (int64_t)S.table.before[P.seg.E] * p_tiles *
-                        (kMode == kGrad ? (P.nq + BQ - 1) / BQ : 1);
+  const int units = S.table.before[P.seg.E] * p_tiles;
 
   auto fail = [&] {
     *abort = 1;
@@ -305,60 +390,72 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < 4) {
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
+      if (elect_one()) {
       // ---------------------------------------------------------- producer
       const uint64_t pol_stream = policy_evict_first(), pol_keep = policy_evict_normal();
       const uint32_t lead_full = mapa_shared(bar_full, 0);
-      int stage = 0;
-      uint32_t phase = 0;
+      Ring ring;
       bool ok = true;
+      // One slot filled by `load(destination, barrier, pair)`: counted on the even CTA's
+      // barrier, or (tail) on this CTA's own, for its tail warp.
+      auto fill = [&](uint32_t bytes, bool tail, auto load) {
+        if (!wait(bar_empty + 8 * ring.slot, ring.phase ^ 1, kWaitLimitNs)) {
+          ok = false;
+          return;
+        }
+        const uint32_t dst = s_slots + ring.slot * kSlotBytes;
+        if (tail) {
+          const uint32_t bar = bar_tail + 8 * ring.slot;
+          mbar_arrive_expect_tx(bar, bytes);
+          load(dst, bar, false);
+        } else {
+          if (rank == 0)
+            mbar_arrive_expect_tx(bar_full + 8 * ring.slot, 2 * bytes);
+          else if (kMode == kGrad)
+            mbar_arrive_remote(lead_full + 8 * ring.slot);
+          load(dst, lead_full + 8 * ring.slot, true);
+        }
+        ring.next();
+      };
+      auto box = [&](uint32_t dst, const CUtensorMap *map, uint32_t bar, bool pair, int x, int y,
+                     int z, uint64_t policy) {
+        if (kMode != kGrad || pair)
+          tma_load_3d_pair(dst, map, bar, x, y, z, policy);
+        else
+          tma_load_3d(dst, map, bar, x, y, z, policy);
+      };
       for (int seq = 0; ok; ++seq) {
         Unit U;
         if (!take(seq, U)) break;
         release_unit(seq);
         if (U.end) break;
         const uint64_t pol_p = U.once ? pol_stream : pol_keep;
-        const int half = U.n / 2;
-        const int boxes = kQMn ? half / 64 : (half + (int)kBoxRows - 1) / (int)kBoxRows;
-        const uint32_t bytes = kPBytes + boxes * (kQMn ? 8192u : kBoxRows * 128u);
-        const int p0 = U.p0 + 128 * rank, q0 = U.q0 + half * rank;
-        for (int b = 0; b < U.blocks; ++b) {
-          if (!wait(bar_empty + 8 * stage, phase ^ 1, kWaitLimitNs)) {
-            ok = false;
-            break;
-          }
-          const uint32_t dp = s_p + stage * kPBytes, dq = s_q + stage * kQBytes;
+        const int p0 = U.p0 + 128 * rank;
+        for (int b = 0; b < U.blocks && ok; ++b) {
           const int t = U.t0 + b * BT;
           const bool tail = kMode == kGrad && b == U.blocks - 1 && (U.rem & 15);
-          if (tail) {
-            // completes here, for the tail warp
-            const uint32_t bar = bar_tail + 8 * stage;
-            mbar_arrive_expect_tx(bar, bytes);
-            for (int j = 0; j < 2; ++j) tma_load_3d(dp + 8192 * j, &tmP, bar, p0 + 64 * j, t, 0, pol_keep);
-            for (int j = 0; j < boxes; ++j)
-              tma_load_3d(dq + 8192 * j, &tmQ, bar, q0 + 64 * j, t, 0, pol_keep);
-          } else {
-            const uint32_t bar = lead_full + 8 * stage;
-            if (rank == 0)
-              mbar_arrive_expect_tx(bar_full + 8 * stage, 2 * bytes);
-            else if (kMode == kGrad)
-              mbar_arrive_cluster(bar);
+          fill(kSlotBytes, tail, [&](uint32_t dst, uint32_t bar, bool pair) {
             if constexpr (kMode == kFwd) {
-              tma_load_3d_pair(dp, &tmP, bar, t, p0, U.z, pol_p);
+              box(dst, &tmP, bar, pair, t, p0, U.z, pol_p);
             } else {
               for (int j = 0; j < 2; ++j)
-                tma_load_3d_pair(dp + 8192 * j, &tmP, bar, p0 + 64 * j, t, kMode == kGrad ? 0 : U.z, pol_p);
+                box(dst + 8192 * j, &tmP, bar, pair, p0 + 64 * j, t, kMode == kGrad ? 0 : U.z, pol_p);
             }
-            for (int j = 0; j < boxes; ++j) {
-              if constexpr (kQMn)
-                tma_load_3d_pair(dq + 8192 * j, &tmQ, bar, q0 + 64 * j, t, 0, pol_keep);
-              else
-                tma_load_3d_pair(dq + kBoxRows * 128 * j, &tmQ, bar, t, q0 + (int)kBoxRows * j, 0, pol_keep);
-            }
-          }
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
+          });
+          for (int a = 0; a < 2 && ok && U.n[a]; ++a) {
+            const int half = U.n[a] / 2, q0 = U.q0 + (a ? U.n[0] : 0) + half * rank;
+            const int boxes = kQMn ? half / 64 : (half + (int)kBoxRows - 1) / (int)kBoxRows;
+            fill(boxes * (kQMn ? 8192u : kBoxRows * 128u), tail,
+                 [&](uint32_t dst, uint32_t bar, bool pair) {
+                   for (int j = 0; j < boxes; ++j) {
+                     if constexpr (kQMn)
+                       box(dst + 8192 * j, &tmQ, bar, pair, q0 + 64 * j, t, 0, pol_keep);
+                     else
+                       box(dst + kBoxRows * 128 * j, &tmQ, bar, pair, t, q0 + (int)kBoxRows * j, 0,
+                           pol_keep);
+                   }
+                 });
           }
         }
       }
@@ -367,14 +464,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (globaltimer() - t0 < 1000000ull) {
         }
       }
-    } else if (warp == 1 && lane == 0) {
+      }
+    } else if (warp == 1) {
+      if (elect_one()) {
       // -------------------------------------------------------- MMA issuer
       // binary32 sums; A = P, B = Q, bits 15 / 16: MN-major
       const uint32_t idesc0 = (1u << 4) | ((uint32_t)P.bf16 << 7) | ((uint32_t)P.bf16 << 10) |
                               ((kPMn ? 1u : 0u) << 15) | ((kQMn ? 1u : 0u) << 16) |
                               ((uint32_t)(BP >> 4) << 24);
-      int stage = 0, acc = 0;
-      uint32_t phase = 0;
+      int acc = 0;
+      Ring ring;
       bool ok = true;
       for (int seq = 0; ok; ++seq) {
         Unit U;
@@ -382,44 +481,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         release_unit(seq);
         if (U.end) break;
         if (rank != 0) continue;  // the odd CTA only follows the unit stream
-        const uint32_t idesc = idesc0 | ((uint32_t)(U.n >> 3) << 17);
-        const int sums = sums_of(U);
-        for (int s = 0; s < sums && ok; ++s) {
-          const int buf = acc & 1;
-          const uint32_t d = tmem + 256 * buf;
-          if (!mbar_wait_cluster(bar_acc_empty + 8 * buf, ((uint32_t)(acc >> 1) & 1u) ^ 1u, abort,
-                                 kWaitLimitNs)) {
-            fail();
-            ok = false;
-            break;
-          }
+        const int accs = U.n[1] ? 2 : 1, sums = sums_of(U);
+        for (int s = 0; s < sums && ok; ++s, acc += accs) {
+          for (int a = 0; a < accs && ok; ++a)
+            ok = wait(bar_acc_empty + 8 * ((acc + a) & 1), ((uint32_t)((acc + a) >> 1) & 1u) ^ 1u,
+                      kWaitLimitNs);
+          if (!ok) break;
           tc_fence_after();
           const int b0 = kF32 ? s * kSumBlocks : 0;
           const int b1 = kF32 ? min(U.blocks, b0 + kSumBlocks) : U.blocks;
-          for (int b = b0; b < b1; ++b) {
-            if (!mbar_wait_cluster(bar_full + 8 * stage, phase, abort, kWaitLimitNs)) {
-              fail();
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t sp = s_p + stage * kPBytes, sq = s_q + stage * kQBytes;
+          for (int b = b0; b < b1 && ok; ++b) {
+            const bool tail = kMode == kGrad && b == U.blocks - 1 && (U.rem & 15);
+            auto arrived = [&] {
+              const uint32_t bar = bar_full + 8 * ring.slot;
+              if (!tail) {
+                ok = wait(bar, ring.phase, kWaitLimitNs);
+              } else if (!mbar_wait_cluster(bar, ring.phase, abort, kWaitLimitNs)) {
+                fail();  // the tail warps' zeros, the odd CTA's too, are seen after this wait
+                ok = false;
+              }
+              tc_fence_after();
+              return ok;
+            };
+            if (!arrived()) break;
+            const int p_slot = ring.slot;
+            const uint32_t sp = s_slots + p_slot * kSlotBytes;
             const int steps = b == U.blocks - 1 ? (U.rem + 15) >> 4 : BT / 16;
+            for (int a = 0; a < accs; ++a) {
+              ring.next();
+              if (!arrived()) break;
+              const uint32_t sq = s_slots + ring.slot * kSlotBytes;
+              const uint32_t d = tmem + 256 * ((acc + a) & 1);
+              const uint32_t idesc = idesc0 | ((uint32_t)(U.n[a] >> 3) << 17);
 #pragma unroll
-            for (int j = 0; j < BT / 16; ++j)
-              if (j < steps)
-                mma_pair_f16(d, operand_desc<kPMn>(sp, j), operand_desc<kQMn>(sq, j), idesc,
-                             (b != b0) | (j != 0));
-            tc_commit_pair_mc(bar_empty + 8 * stage, kBoth);
-            if (++stage == kStages) {
-              stage = 0;
-              phase ^= 1;
+              for (int j = 0; j < BT / 16; ++j)
+                if (j < steps)
+                  mma_pair_f16(d, operand_desc<kPMn>(sp, j), operand_desc<kQMn>(sq, j), idesc,
+                               (b != b0) | (j != 0));
+              tc_commit_pair_mc(bar_empty + 8 * ring.slot, kBoth);
             }
+            if (!ok) break;
+            tc_commit_pair_mc(bar_empty + 8 * p_slot, kBoth);
+            ring.next();
           }
           if (!ok) break;
-          tc_commit_pair_mc(bar_acc_full + 8 * buf, kBoth);
-          ++acc;
+          for (int a = 0; a < accs; ++a) tc_commit_pair_mc(bar_acc_full + 8 * ((acc + a) & 1), kBoth);
         }
+      }
       }
     } else if (warp == 2 && lane == 0) {
       // --------------------------------------------------------- scheduler
@@ -434,8 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       bool ok = true;
-      for (int64_t u = cluster_id_x(); ok && u < units; u += cluster_count_x())
-        ok = push(get_unit<kMode>(P, S.table, u, p_tiles));
+      for (int u = cluster_id_x(); ok && u < units; u += cluster_count_x())
+        ok = push(get_unit<kMode, kF32>(P, S.table, u, p_tiles));
       if (ok) {
         Unit end = {};
         end.end = 1;
@@ -444,31 +552,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (kMode == kGrad && warp == 3) {
       // -------------------------------------- rows past the segment's last
       const uint32_t lead_full = mapa_shared(bar_full, 0);
-      int stage = 0;
-      uint32_t parity = 0;  // of each stage's tail barrier
+      int slot = 0;
+      uint32_t parity = 0;  // of each slot's tail barrier
       for (int seq = 0;; ++seq) {
         Unit U;
         if (!take_warp(seq, U)) break;
         __syncwarp();
         if (lane == 0) release_unit(seq);
         if (U.end) break;
+        const int each = U.n[1] ? 3 : 2;  // slots of a block: P, one or two Q
+        bool ok = true;
         if (U.blocks > 0 && (U.rem & 15)) {
-          const int s = (stage + U.blocks - 1) % kStages;
-          if (!wait_warp(bar_tail + 8 * s, (parity >> s) & 1u, unit_limit)) break;
-          parity ^= 1u << s;
-          // 8 pieces of 16 bytes a row, in P's two column blocks and Q's (one or) two
           const int lines = 16 - (U.rem & 15);
-          for (int i = lane; i < lines * 32; i += 32) {
-            const int row = U.rem + (i >> 5), block = (i >> 3) & 3, piece = i & 7;
-            uint8_t *base = smem + (block < 2 ? s * kPBytes : kStages * kPBytes + s * kQBytes);
-            *reinterpret_cast<uint4 *>(base + (block & 1) * 8192 + row * 128 + piece * 16) =
-                make_uint4(0, 0, 0, 0);
+          for (int a = 0; a < each && ok; ++a) {
+            const int s = (int)((slot + (int64_t)(U.blocks - 1) * each + a) % kSlots);
+            ok = wait_warp(bar_tail + 8 * s, (parity >> s) & 1u, unit_limit);
+            if (!ok) break;
+            parity ^= 1u << s;
+            // 8 pieces of 16 bytes a row, in the slot's two column blocks
+            for (int i = lane; i < lines * 16; i += 32) {
+              const int row = U.rem + (i >> 4), block = (i >> 3) & 1, piece = i & 7;
+              *reinterpret_cast<uint4 *>(smem + s * kSlotBytes + block * 8192 + row * 128 +
+                                         piece * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(lead_full + 8 * s);
           }
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead_full + 8 * s);
         }
-        stage = (stage + U.blocks) % kStages;
+        if (!ok) break;
+        slot = (int)((slot + (int64_t)U.blocks * each) % kSlots);
       }
     }
   } else {
@@ -478,6 +591,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t t_lane = tmem + ((uint32_t)(32 * quarter) << 16);
     const uint32_t lead_acc_empty = mapa_shared(bar_acc_empty, 0);
+    uint8_t *stage_ptr = smem + kOffStage + (warp - 4) * kStageBytes;
+    const uint32_t stage = smem_u32(stage_ptr);
     int acc = 0;
     bool ok = true;
     for (int seq = 0; ok; ++seq) {
@@ -486,21 +601,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) release_unit(seq);
       if (U.end) break;
-      const int p = U.p0 + 128 * rank + 32 * quarter + lane;
-      const int64_t pitch = P.np;
-      const int64_t row0 = kMode == kGrad ? (int64_t)U.z * P.nq + U.q0 : U.q0;
-      O *out = static_cast<O *>(P.out) + row0 * pitch;
+      const int pw = U.p0 + 128 * rank + 32 * quarter;  // the warp's first p
       auto release = [&](int buf) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead_acc_empty + 8 * buf);
+        if (lane == 0) mbar_arrive_remote(lead_acc_empty + 8 * buf);
       };
       if constexpr (kF32) {
+        // the sums start at what the output holds (accumulate), loaded while the MMAs run
+        const int p = pw + lane;
+        int64_t pitch = P.np;
+        float *out = static_cast<float *>(P.out) + ((int64_t)U.z * P.nq + U.q0) * pitch + p;
         float sum[4][32];
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+        for (int g = 0; g < 4; ++g) {
+          const int c = 32 * (half + 2 * g);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) sum[g][j] = 0.0f;
+          for (int j = 0; j < 32; ++j)
+            sum[g][j] = P.accumulate && p < P.np && c + j < U.nq ? out[(c + j) * pitch] : 0.0f;
+        }
         const int sums = sums_of(U);
         for (int s = 0; s < sums; ++s, ++acc) {
           const int buf = acc & 1;
@@ -528,39 +647,59 @@ __global__ void __launch_bounds__(kThreads, 1)
           release(buf);
         }
         if (!ok) break;
+        asm volatile("" : "+l"(pitch));  // the addresses again, not 128 of them kept
+        if (p < P.np) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int c = 32 * (half + 2 * g);
-          if (c >= U.nq || p >= P.np) continue;
-          float *o = reinterpret_cast<float *>(out) + (int64_t)c * pitch + p;
-          if (P.accumulate) {
+          for (int g = 0; g < 4; ++g) {
+            const int c = 32 * (half + 2 * g);
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (c + j < U.nq) sum[g][j] += o[(int64_t)j * pitch];
+              if (c + j < U.nq) out[(c + j) * pitch] = sum[g][j];
           }
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c + j < U.nq) o[(int64_t)j * pitch] = sum[g][j];
         }
       } else {
-        const int buf = acc & 1;
-        if (!wait_warp(bar_acc_full + 8 * buf, (uint32_t)(acc >> 1) & 1u, unit_limit)) break;
-        ++acc;
-        tc_fence_after();
-        for (int c = 32 * half; c < U.nq; c += 64) {
-          uint32_t v[32];
-          MOE_TMEM_LD_32x32b_X32(t_lane + 256 * buf + c, v);
-          tc_wait_ld();
-          if (U.blocks == 0) {  // a segment without rows: nothing was accumulated
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0;
+        const int accs = U.n[1] ? 2 : 1;
+        for (int a = 0; a < accs; ++a, ++acc) {
+          const int buf = acc & 1;
+          if (!wait_warp(bar_acc_full + 8 * buf, (uint32_t)(acc >> 1) & 1u, unit_limit)) {
+            ok = false;
+            break;
           }
-          store_columns<O>(v, reinterpret_cast<uint16_t *>(out) + (int64_t)c * pitch, pitch, p, P.np,
-                           U.nq - c, lane);
+          tc_fence_after();
+          const int q0 = a ? U.n[0] : 0, nq = a ? U.nq - U.n[0] : min(U.nq, U.n[0]);
+          for (int c = 32 * half; c < nq; c += 64) {
+            if (elect_one()) bulk_wait_read();  // the staging block's last copy has left it
+            __syncwarp();
+            stage_block<O>(t_lane + 256 * buf + c, U.blocks == 0, stage, lane);
+            const int row = U.q0 + q0 + c;
+            if (kMode == kGrad || nq - c >= 32) {
+              // all 32 q's are stored (the gradient's map ends at its last q)
+              fence_async_shared();
+              __syncwarp();
+              if (pw < P.np && elect_one()) {
+                tma_store_3d(&tmO, stage, pw, row, kMode == kGrad ? U.z : 0);
+                bulk_commit();
+              }
+            } else {
+              // a segment's last rows: what follows belongs to another
+              __syncwarp();
+              const int piece = lane & 3;
+              uint16_t *out = static_cast<uint16_t *>(P.out) + (int64_t)row * P.np + pw + 8 * piece;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int q = 8 * i + (lane >> 2);
+                const uint4 x = *reinterpret_cast<const uint4 *>(stage_ptr + stage_offset(q, piece));
+                if (q < nq - c && pw + 8 * piece < P.np)
+                  *reinterpret_cast<uint4 *>(out + (int64_t)q * P.np) = x;
+              }
+              __syncwarp();
+            }
+          }
+          release(buf);
         }
-        release(buf);
       }
     }
+    if (!kF32 && elect_one()) bulk_wait();
   }
 
   tc_fence_before();
@@ -589,17 +728,19 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 16-bit tensor [mats][rows][cols] (cols contiguous), boxes of box_rows x 64 columns.
+// 16-bit tensor [mats][rows][cols] (cols contiguous), boxes of box_rows x box_cols, the
+// rows of a box (128 or 64 bytes) swizzled.
 bool make_map(CUtensorMap *m, const void *base, uint64_t mats, uint64_t rows, uint64_t cols,
-              uint32_t box_rows) {
+              uint32_t box_rows, uint32_t box_cols = BT) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {cols, rows, mats};
   cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
-  cuuint32_t box[3] = {BT, box_rows, 1};
+  cuuint32_t box[3] = {box_cols, box_rows, 1};
   cuuint32_t es[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box_cols == BT ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -617,8 +758,8 @@ bool off16(const void *p) { return (uintptr_t)p % 16 != 0; }
 
 // max_units: no more units than this (the grid need not be larger).
 template <int kMode, class O>
-int launch(const CUtensorMap &mp, const CUtensorMap &mq, const GroupedParams &P, int64_t max_units,
-           int num_sms, void *stream) {
+int launch(const CUtensorMap &mp, const CUtensorMap &mq, const CUtensorMap &mo,
+           const GroupedParams &P, int64_t max_units, int num_sms, void *stream) {
   static int max_clusters[kMaxDevices] = {};
   const int dev = device_slot();
   if (dev < 0) return dev;
@@ -650,7 +791,7 @@ int launch(const CUtensorMap &mp, const CUtensorMap &mq, const GroupedParams &P,
   if (clusters > max_units) clusters = max_units;
   if (clusters < 1) return MOE_OK;
   cfg.gridDim = dim3((unsigned)(2 * clusters));
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, mp, mq, P);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, mp, mq, mo, P);
   if (e != cudaSuccess) return set_cuda_error(e);
   return check_launch();
 }
@@ -673,19 +814,21 @@ extern "C" int moe_grouped_gemm(const moe_ggemm_args *a, void *stream) {
   P.nt = a->trans ? a->n : a->k;
   P.bf16 = a->type == MOE_TYPE_BF16;
   P.out = a->out;
-  CUtensorMap mp, mq;
+  CUtensorMap mp, mq, mo;
   if (!make_map(&mp, a->w, (uint64_t)a->seg.E, (uint64_t)a->n, (uint64_t)a->k, a->trans ? BT : 128) ||
-      !make_map(&mq, a->x, 1, (uint64_t)a->seg.rows, (uint64_t)P.nt, kBoxRows))
+      !make_map(&mq, a->x, 1, (uint64_t)a->seg.rows, (uint64_t)P.nt, kBoxRows) ||
+      !make_map(&mo, a->out, 1, (uint64_t)a->seg.rows, (uint64_t)P.np, 32, 32))
     return MOE_ERR_CUDA;
-  // row tiles: a full one per 256 rows, and one started in every segment that has rows
+  // row tiles: a full one per 512 rows, and one started in every segment that has rows
   const int64_t started = a->seg.E < a->seg.rows ? a->seg.E : a->seg.rows;
-  const int64_t max_units = (a->seg.rows / BQ + started) * ((P.np + BP - 1) / BP);
+  const int64_t max_units = (a->seg.rows / kWide + started) * ((P.np + BP - 1) / BP);
+  if (max_units > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   const bool bf = P.bf16;
   if (a->trans)
-    return bf ? launch<kTrans, __nv_bfloat16>(mp, mq, P, max_units, a->num_sms, stream)
-              : launch<kTrans, __half>(mp, mq, P, max_units, a->num_sms, stream);
-  return bf ? launch<kFwd, __nv_bfloat16>(mp, mq, P, max_units, a->num_sms, stream)
-            : launch<kFwd, __half>(mp, mq, P, max_units, a->num_sms, stream);
+    return bf ? launch<kTrans, __nv_bfloat16>(mp, mq, mo, P, max_units, a->num_sms, stream)
+              : launch<kTrans, __half>(mp, mq, mo, P, max_units, a->num_sms, stream);
+  return bf ? launch<kFwd, __nv_bfloat16>(mp, mq, mo, P, max_units, a->num_sms, stream)
+            : launch<kFwd, __half>(mp, mq, mo, P, max_units, a->num_sms, stream);
 }
 
 extern "C" int moe_grouped_wgrad(const moe_wgrad_args *a, void *stream) {
@@ -706,14 +849,16 @@ extern "C" int moe_grouped_wgrad(const moe_wgrad_args *a, void *stream) {
   P.accumulate = a->accumulate != 0;
   // without rows every segment is empty: the maps are not used, and need only be valid
   const uint64_t rows = a->seg.rows > 0 ? (uint64_t)a->seg.rows : 1;
-  CUtensorMap mp, mq;
+  CUtensorMap mp, mq, mo;
   if (!make_map(&mp, a->seg.rows > 0 ? a->x : a->out, 1, rows, (uint64_t)a->k, BT) ||
-      !make_map(&mq, a->seg.rows > 0 ? a->dy : a->out, 1, rows, (uint64_t)a->n, BT))
+      !make_map(&mq, a->seg.rows > 0 ? a->dy : a->out, 1, rows, (uint64_t)a->n, BT) ||
+      !make_map(&mo, a->out, (uint64_t)a->seg.E, (uint64_t)a->n, (uint64_t)a->k, 32, 32))
     return MOE_ERR_CUDA;
   const int64_t max_units =
       (int64_t)a->seg.E * ((a->k + BP - 1) / BP) * ((a->n + BQ - 1) / BQ);
+  if (max_units > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (a->out_type == MOE_TYPE_F32)
-    return launch<kGrad, float>(mp, mq, P, max_units, a->num_sms, stream);
-  return P.bf16 ? launch<kGrad, __nv_bfloat16>(mp, mq, P, max_units, a->num_sms, stream)
-                : launch<kGrad, __half>(mp, mq, P, max_units, a->num_sms, stream);
+    return launch<kGrad, float>(mp, mq, mo, P, max_units, a->num_sms, stream);
+  return P.bf16 ? launch<kGrad, __nv_bfloat16>(mp, mq, mo, P, max_units, a->num_sms, stream)
+                : launch<kGrad, __half>(mp, mq, mo, P, max_units, a->num_sms, stream);
 }
