@@ -32,6 +32,8 @@
 // the epilogue's registers with rounding to nearest.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "segments.cuh"
 
 namespace moe {
@@ -41,10 +43,13 @@ constexpr int kFwd = 0, kTrans = 1, kGrad = 2;
 constexpr int kThreads = 384, kEpiWarps = 8;
 constexpr int BP = 256, BQ = 256, BT = 64;  // tile of a CTA pair, depth of a block of t
 constexpr int kWide = 2 * BQ;               // q's of a wide unit
-constexpr int kSlots = 12, kUnitQ = 8;
+constexpr int kUnitQ = 8;
 constexpr uint32_t kSlotBytes = 128 * BT * 2;  // a CTA's half of a P or Q tile
-constexpr uint32_t kBoxRows = 32;              // rows of one Q box
-constexpr uint32_t kStageBytes = 32 * 64;      // an epilogue warp's 32 x 32 16-bit block
+// Slots of the operand ring, and an epilogue warp's staging: a 32 x 32 block of 16-bit
+// values, or two 16 x 32 blocks of binary32 ones.
+constexpr int slots_of(bool f32) { return f32 ? 10 : 12; }
+constexpr uint32_t stage_bytes(bool f32) { return f32 ? 2 * 2048 : 2048; }
+constexpr int kMaxDepth = 6;  // blocks in the ring: half the slots
 constexpr int kSumBlocks = 8;  // blocks of one partial sum (binary32 output): 512 rows
 constexpr int kWideRows = 1024;  // rows from which the gradient takes wide units
 constexpr uint32_t kTmemCols = 512;
@@ -63,20 +68,29 @@ struct Unit {
   int end;
 };
 
-// A place in the ring of operand slots.
+// The operand ring: block i of the CTA's stream takes two or three consecutive slots (P,
+// and a Q for each accumulator) and the barriers i % kDepth.  Every role that follows the
+// stream keeps such a place.
+template <int kSlots>
 struct Ring {
-  int slot = 0;
+  int slot = 0, bar = 0;
   uint32_t phase = 0;
-  __device__ __forceinline__ void next() {
-    if (++slot == kSlots) {
-      slot = 0;
+  __device__ __forceinline__ uint32_t at(int a) const {  // byte offset of the block's slot a
+    const int s = slot + a;
+    return (uint32_t)(s >= kSlots ? s - kSlots : s) * kSlotBytes;
+  }
+  __device__ __forceinline__ void next(int width) {
+    slot += width;
+    if (slot >= kSlots) slot -= kSlots;
+    if (++bar == kSlots / 2) {
+      bar = 0;
       phase ^= 1;
     }
   }
 };
 
 struct Shared {
-  uint64_t full[kSlots], empty[kSlots], tail[kSlots];
+  uint64_t full[kMaxDepth], empty[kMaxDepth], tail[kMaxDepth], peer[kMaxDepth];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t unit_full[kUnitQ], unit_empty[kUnitQ];
   Unit unit[kUnitQ];
@@ -85,35 +99,45 @@ struct Shared {
   long long part[33];
   SegTable table;
 };
-constexpr uint32_t kOffStage = kSlots * kSlotBytes;
-constexpr uint32_t kOffShared = kOffStage + kEpiWarps * kStageBytes;
-constexpr uint32_t kSmemBytes = kOffShared + sizeof(Shared) + 1024;
-static_assert(kSmemBytes <= 232448, "shared memory");
+constexpr uint32_t off_stage(bool f32) { return slots_of(f32) * kSlotBytes; }
+constexpr uint32_t off_shared(bool f32) { return off_stage(f32) + kEpiWarps * stage_bytes(f32); }
+constexpr uint32_t smem_bytes(bool f32) { return off_shared(f32) + sizeof(Shared) + 1024; }
+static_assert(smem_bytes(false) <= 232448 && smem_bytes(true) <= 232448, "shared memory");
+
+// An MN-major operand's column blocks of 64 are a dimension of its map where the columns
+// are a multiple of 64 (`blocked`: one copy brings two blocks), else one copy each.
+struct Maps {
+  CUtensorMap p;
+  CUtensorMap q[8];  // K-major: boxes of 16, 32, ..., 128 rows; MN-major: of 1, 2 blocks
+  CUtensorMap out;
+};
 
 struct GroupedParams {
   SegParams seg;
   int np, nq, nt;  // extents of p; of q (gradient: n); of t (forward, trans)
+  int p_blocked, q_blocked;
   int bf16;
   int accumulate;
   void *out;
 };
 
 // ----------------------------------------------------------------------- PTX
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void *map, uint32_t bar,
-                                                 int x, int y, int z, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile"
-      ".mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, uint32_t bar, int x,
-                                            int y, int z, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile"
-      ".mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
-      : "memory");
+// Copies of one box: counted on the even CTA's barrier, or (kPair false) on this CTA's.
+template <bool kPair>
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x,
+                                         int y, int c, int z, uint64_t policy) {
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(c), "r"(z), "l"(policy)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(c), "r"(z), "l"(policy)
+        : "memory");
 }
 // D (+)= A B^T over the pair: 256 rows of A (128 per CTA), N of B (half per CTA).
 __device__ __forceinline__ void mma_pair_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
@@ -172,15 +196,26 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(p));
   return p != 0;
 }
-__device__ __forceinline__ void tma_store_3d(const void *map, uint32_t src, int x, int y, int z) {
+__device__ __forceinline__ void tma_store(const void *map, uint32_t src, int x, int y, int z) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
-      "r"(src), "r"(x), "r"(y), "r"(z)
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %5, %4}], [%1];" ::"l"(map),
+      "r"(src), "r"(x), "r"(y), "r"(z), "r"(0)
+      : "memory");
+}
+__device__ __forceinline__ void tma_add(const void *map, uint32_t src, int x, int y, int z) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.4d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %5, %4}], "
+      "[%1];" ::"l"(map),
+      "r"(src), "r"(x), "r"(y), "r"(z), "r"(0)
       : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// The thread's bulk stores have read their shared memory / are complete.
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// All of the thread's bulk stores but the last kBut have read their shared memory / all
+// are complete.
+template <int kBut>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBut) : "memory");
+}
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -293,18 +328,18 @@ __device__ __forceinline__ void stage_block(uint32_t taddr, bool zero, uint32_t 
 
 template <int kMode, class O>
 __global__ void __launch_bounds__(kThreads, 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
-                   const __grid_constant__ CUtensorMap tmO, const GroupedParams P) {
+    grouped_kernel(const __grid_constant__ Maps M, const GroupedParams P) {
   constexpr bool kF32 = sizeof(O) == 4;
+  constexpr int kSlots = slots_of(kF32);
   constexpr bool kPMn = kMode != kFwd, kQMn = kMode == kGrad;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Shared &S = *reinterpret_cast<Shared *>(smem + kOffShared);
+  Shared &S = *reinterpret_cast<Shared *>(smem + off_shared(kF32));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t s_slots = smem_u32(smem);
   const uint32_t bar_full = smem_u32(S.full), bar_empty = smem_u32(S.empty);
-  const uint32_t bar_tail = smem_u32(S.tail);
+  const uint32_t bar_tail = smem_u32(S.tail), bar_peer = smem_u32(S.peer);
   const uint32_t bar_acc_full = smem_u32(S.acc_full), bar_acc_empty = smem_u32(S.acc_empty);
   const uint32_t bar_unit_full = smem_u32(S.unit_full), bar_unit_empty = smem_u32(S.unit_empty);
   volatile int *abort = &S.abort;
@@ -312,10 +347,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rank = (int)cluster_ctarank();
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(bar_full + 8 * s, kMode == kGrad ? 2 : 1);  // gradient: each CTA arrives
+    for (int s = 0; s < kMaxDepth; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
       mbar_init(bar_tail + 8 * s, 1);
+      mbar_init(bar_peer + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar_acc_full + 8 * b, 1);
@@ -328,9 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     S.abort = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tmP);
-    tma_prefetch_desc(&tmQ);
-    if (!kF32) tma_prefetch_desc(&tmO);
+    tma_prefetch_desc(&M.p);
+    tma_prefetch_desc(&M.out);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(&S.tmem), kTmemCols);
@@ -395,68 +430,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- producer
       const uint64_t pol_stream = policy_evict_first(), pol_keep = policy_evict_normal();
       const uint32_t lead_full = mapa_shared(bar_full, 0);
-      Ring ring;
+      Ring<kSlots> ring, oldest;  // the block to fill, and the oldest not known to be free
+      int free = kSlots, blocks = 0;
+      uint32_t wide = 0;          // bit i: block i after the oldest takes three slots
       bool ok = true;
-      // One slot filled by `load(destination, barrier, pair)`: counted on the even CTA's
-      // barrier, or (tail) on this CTA's own, for its tail warp.
-      auto fill = [&](uint32_t bytes, bool tail, auto load) {
-        if (!wait(bar_empty + 8 * ring.slot, ring.phase ^ 1, kWaitLimitNs)) {
-          ok = false;
-          return;
-        }
-        const uint32_t dst = s_slots + ring.slot * kSlotBytes;
-        if (tail) {
-          const uint32_t bar = bar_tail + 8 * ring.slot;
-          mbar_arrive_expect_tx(bar, bytes);
-          load(dst, bar, false);
-        } else {
-          if (rank == 0)
-            mbar_arrive_expect_tx(bar_full + 8 * ring.slot, 2 * bytes);
-          else if (kMode == kGrad)
-            mbar_arrive_remote(lead_full + 8 * ring.slot);
-          load(dst, lead_full + 8 * ring.slot, true);
-        }
-        ring.next();
-      };
-      auto box = [&](uint32_t dst, const CUtensorMap *map, uint32_t bar, bool pair, int x, int y,
-                     int z, uint64_t policy) {
-        if (kMode != kGrad || pair)
-          tma_load_3d_pair(dst, map, bar, x, y, z, policy);
-        else
-          tma_load_3d(dst, map, bar, x, y, z, policy);
-      };
       for (int seq = 0; ok; ++seq) {
         Unit U;
         if (!take(seq, U)) break;
         release_unit(seq);
         if (U.end) break;
         const uint64_t pol_p = U.once ? pol_stream : pol_keep;
-        const int p0 = U.p0 + 128 * rank;
-        for (int b = 0; b < U.blocks && ok; ++b) {
+        const int p0 = U.p0 + 128 * rank, width = U.n[1] ? 3 : 2;
+        int half[2], q0[2];
+        for (int a = 0; a < 2; ++a) {
+          half[a] = U.n[a] / 2;
+          q0[a] = U.q0 + (a ? U.n[0] : 0) + half[a] * rank;
+        }
+        const uint32_t bytes = kSlotBytes + (half[0] + half[1]) * (BT * 2);  // of this CTA
+        for (int b = 0; b < U.blocks; ++b) {
+          while (ok && (free < width || blocks == kSlots / 2)) {
+            ok = wait(bar_empty + 8 * oldest.bar, oldest.phase, kWaitLimitNs);
+            free += 2 + (wide & 1);
+            wide >>= 1;
+            --blocks;
+            oldest.next(0);
+          }
+          if (!ok) break;
           const int t = U.t0 + b * BT;
-          const bool tail = kMode == kGrad && b == U.blocks - 1 && (U.rem & 15);
-          fill(kSlotBytes, tail, [&](uint32_t dst, uint32_t bar, bool pair) {
+          auto load = [&](auto pair, uint32_t bar) {
+            constexpr bool kPair = decltype(pair)::value;
+            const uint32_t dp = s_slots + ring.at(0);
             if constexpr (kMode == kFwd) {
-              box(dst, &tmP, bar, pair, t, p0, U.z, pol_p);
+              tma_load<kPair>(dp, &M.p, bar, t, p0, 0, U.z, pol_p);
+            } else if (P.p_blocked) {
+              tma_load<kPair>(dp, &M.p, bar, 0, t, p0 >> 6, kMode == kGrad ? 0 : U.z, pol_p);
             } else {
               for (int j = 0; j < 2; ++j)
-                box(dst + 8192 * j, &tmP, bar, pair, p0 + 64 * j, t, kMode == kGrad ? 0 : U.z, pol_p);
+                tma_load<kPair>(dp + 8192 * j, &M.p, bar, p0 + 64 * j, t, 0,
+                                kMode == kGrad ? 0 : U.z, pol_p);
             }
-          });
-          for (int a = 0; a < 2 && ok && U.n[a]; ++a) {
-            const int half = U.n[a] / 2, q0 = U.q0 + (a ? U.n[0] : 0) + half * rank;
-            const int boxes = kQMn ? half / 64 : (half + (int)kBoxRows - 1) / (int)kBoxRows;
-            fill(boxes * (kQMn ? 8192u : kBoxRows * 128u), tail,
-                 [&](uint32_t dst, uint32_t bar, bool pair) {
-                   for (int j = 0; j < boxes; ++j) {
-                     if constexpr (kQMn)
-                       box(dst + 8192 * j, &tmQ, bar, pair, q0 + 64 * j, t, 0, pol_keep);
-                     else
-                       box(dst + kBoxRows * 128 * j, &tmQ, bar, pair, t, q0 + (int)kBoxRows * j, 0,
-                           pol_keep);
-                   }
-                 });
+            for (int a = 0; a < width - 1; ++a) {
+              const uint32_t dq = s_slots + ring.at(1 + a);
+              if constexpr (!kQMn) {
+                tma_load<kPair>(dq, &M.q[half[a] / 16 - 1], bar, t, q0[a], 0, 0, pol_keep);
+              } else if (P.q_blocked) {
+                tma_load<kPair>(dq, &M.q[half[a] / 64 - 1], bar, 0, t, q0[a] >> 6, 0, pol_keep);
+              } else {
+                for (int j = 0; j < half[a] / 64; ++j)
+                  tma_load<kPair>(dq + 8192 * j, &M.q[0], bar, q0[a] + 64 * j, t, 0, 0, pol_keep);
+              }
+            }
+          };
+          if (kMode == kGrad && b == U.blocks - 1 && (U.rem & 15)) {
+            // completes in this CTA, for its tail warp
+            mbar_arrive_expect_tx(bar_tail + 8 * ring.bar, bytes);
+            load(std::false_type{}, bar_tail + 8 * ring.bar);
+          } else {
+            if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * ring.bar, 2 * bytes);
+            load(std::true_type{}, lead_full + 8 * ring.bar);
           }
+          free -= width;
+          wide |= (uint32_t)(width - 2) << blocks;
+          ++blocks;
+          ring.next(width);
         }
       }
       if (*abort) {  // let the copies in flight land before the CTA can exit
@@ -473,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                               ((kPMn ? 1u : 0u) << 15) | ((kQMn ? 1u : 0u) << 16) |
                               ((uint32_t)(BP >> 4) << 24);
       int acc = 0;
-      Ring ring;
+      Ring<kSlots> ring;
       bool ok = true;
       for (int seq = 0; ok; ++seq) {
         Unit U;
@@ -491,26 +527,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int b0 = kF32 ? s * kSumBlocks : 0;
           const int b1 = kF32 ? min(U.blocks, b0 + kSumBlocks) : U.blocks;
           for (int b = b0; b < b1 && ok; ++b) {
-            const bool tail = kMode == kGrad && b == U.blocks - 1 && (U.rem & 15);
-            auto arrived = [&] {
-              const uint32_t bar = bar_full + 8 * ring.slot;
-              if (!tail) {
-                ok = wait(bar, ring.phase, kWaitLimitNs);
-              } else if (!mbar_wait_cluster(bar, ring.phase, abort, kWaitLimitNs)) {
-                fail();  // the tail warps' zeros, the odd CTA's too, are seen after this wait
-                ok = false;
-              }
-              tc_fence_after();
-              return ok;
-            };
-            if (!arrived()) break;
-            const int p_slot = ring.slot;
-            const uint32_t sp = s_slots + p_slot * kSlotBytes;
+            ok = wait(bar_full + 8 * ring.bar, ring.phase, kWaitLimitNs);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sp = s_slots + ring.at(0);
             const int steps = b == U.blocks - 1 ? (U.rem + 15) >> 4 : BT / 16;
             for (int a = 0; a < accs; ++a) {
-              ring.next();
-              if (!arrived()) break;
-              const uint32_t sq = s_slots + ring.slot * kSlotBytes;
+              const uint32_t sq = s_slots + ring.at(1 + a);
               const uint32_t d = tmem + 256 * ((acc + a) & 1);
               const uint32_t idesc = idesc0 | ((uint32_t)(U.n[a] >> 3) << 17);
 #pragma unroll
@@ -518,11 +541,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (j < steps)
                   mma_pair_f16(d, operand_desc<kPMn>(sp, j), operand_desc<kQMn>(sq, j), idesc,
                                (b != b0) | (j != 0));
-              tc_commit_pair_mc(bar_empty + 8 * ring.slot, kBoth);
             }
-            if (!ok) break;
-            tc_commit_pair_mc(bar_empty + 8 * p_slot, kBoth);
-            ring.next();
+            tc_commit_pair_mc(bar_empty + 8 * ring.bar, kBoth);
+            ring.next(1 + accs);
           }
           if (!ok) break;
           for (int a = 0; a < accs; ++a) tc_commit_pair_mc(bar_acc_full + 8 * ((acc + a) & 1), kBoth);
@@ -551,37 +572,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (kMode == kGrad && warp == 3) {
       // -------------------------------------- rows past the segment's last
-      const uint32_t lead_full = mapa_shared(bar_full, 0);
-      int slot = 0;
-      uint32_t parity = 0;  // of each slot's tail barrier
+      const uint32_t lead_peer = mapa_shared(bar_peer, 0);
+      int64_t slot = 0, block = 0;
+      uint32_t parity = 0;  // of each tail and peer barrier
       for (int seq = 0;; ++seq) {
         Unit U;
         if (!take_warp(seq, U)) break;
         __syncwarp();
         if (lane == 0) release_unit(seq);
         if (U.end) break;
-        const int each = U.n[1] ? 3 : 2;  // slots of a block: P, one or two Q
-        bool ok = true;
-        if (U.blocks > 0 && (U.rem & 15)) {
-          const int lines = 16 - (U.rem & 15);
-          for (int a = 0; a < each && ok; ++a) {
-            const int s = (int)((slot + (int64_t)(U.blocks - 1) * each + a) % kSlots);
-            ok = wait_warp(bar_tail + 8 * s, (parity >> s) & 1u, unit_limit);
-            if (!ok) break;
-            parity ^= 1u << s;
-            // 8 pieces of 16 bytes a row, in the slot's two column blocks
-            for (int i = lane; i < lines * 16; i += 32) {
-              const int row = U.rem + (i >> 4), block = (i >> 3) & 1, piece = i & 7;
-              *reinterpret_cast<uint4 *>(smem + s * kSlotBytes + block * 8192 + row * 128 +
-                                         piece * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(lead_full + 8 * s);
+        const int width = U.n[1] ? 3 : 2;
+        slot += (int64_t)U.blocks * width;  // after the unit
+        block += U.blocks;
+        if (U.blocks == 0 || (U.rem & 15) == 0) continue;
+        const int bar = (int)((block - 1) % (kSlots / 2));
+        if (!wait_warp(bar_tail + 8 * bar, (parity >> bar) & 1u, unit_limit)) break;
+        // 8 pieces of 16 bytes a row, in the two column blocks of each slot
+        const int lines = 16 - (U.rem & 15);
+        for (int a = 0; a < width; ++a) {
+          uint8_t *base = smem + (slot - width + a) % kSlots * kSlotBytes;
+          for (int i = lane; i < lines * 16; i += 32) {
+            const int row = U.rem + (i >> 4), half = (i >> 3) & 1, piece = i & 7;
+            *reinterpret_cast<uint4 *>(base + half * 8192 + row * 128 + piece * 16) =
+                make_uint4(0, 0, 0, 0);
           }
         }
-        if (!ok) break;
-        slot = (int)((slot + (int64_t)U.blocks * each) % kSlots);
+        fence_async_shared();
+        __syncwarp();
+        // the odd CTA's zeros are known to the even one's warp, which then opens the block
+        if (rank == 1) {
+          if (lane == 0) mbar_arrive_cluster(lead_peer + 8 * bar);
+        } else {
+          const bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar_peer + 8 * bar, (parity >> bar) & 1u,
+                                                                    abort, unit_limit));
+          if (!ok) {
+            fail();
+            break;
+          }
+          if (lane == 0) mbar_arrive(bar_full + 8 * bar);
+        }
+        parity ^= 1u << bar;
       }
     }
   } else {
@@ -591,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t t_lane = tmem + ((uint32_t)(32 * quarter) << 16);
     const uint32_t lead_acc_empty = mapa_shared(bar_acc_empty, 0);
-    uint8_t *stage_ptr = smem + kOffStage + (warp - 4) * kStageBytes;
+    uint8_t *stage_ptr = smem + off_stage(kF32) + (warp - 4) * stage_bytes(kF32);
     const uint32_t stage = smem_u32(stage_ptr);
     int acc = 0;
     bool ok = true;
@@ -608,18 +638,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_remote(lead_acc_empty + 8 * buf);
       };
       if constexpr (kF32) {
-        // the sums start at what the output holds (accumulate), loaded while the MMAs run
-        const int p = pw + lane;
-        int64_t pitch = P.np;
-        float *out = static_cast<float *>(P.out) + ((int64_t)U.z * P.nq + U.q0) * pitch + p;
         float sum[4][32];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int c = 32 * (half + 2 * g);
+        for (int g = 0; g < 4; ++g)
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            sum[g][j] = P.accumulate && p < P.np && c + j < U.nq ? out[(c + j) * pitch] : 0.0f;
-        }
+          for (int j = 0; j < 32; ++j) sum[g][j] = 0.0f;
         const int sums = sums_of(U);
         for (int s = 0; s < sums; ++s, ++acc) {
           const int buf = acc & 1;
@@ -647,14 +670,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           release(buf);
         }
         if (!ok) break;
-        asm volatile("" : "+l"(pitch));  // the addresses again, not 128 of them kept
-        if (p < P.np) {
+        // 16 q's x 32 p at a time through the warp's two staging blocks; with accumulate the
+        // copy adds to the output in L2 (each value once, so in no particular order)
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int c = 32 * (half + 2 * g);
+        for (int g = 0; g < 4; ++g) {
+          const int c = 32 * (half + 2 * g);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < U.nq) out[(c + j) * pitch] = sum[g][j];
+          for (int h = 0; h < 2; ++h) {
+            if (c + 16 * h < U.nq) {
+              if (elect_one()) bulk_wait_read<1>();
+              __syncwarp();
+              float *row = reinterpret_cast<float *>(stage_ptr + h * 2048) + lane;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) row[32 * j] = sum[g][16 * h + j];
+              fence_async_shared();
+              __syncwarp();
+              if (pw < P.np && elect_one()) {
+                if (P.accumulate)
+                  tma_add(&M.out, stage + h * 2048, pw, U.q0 + c + 16 * h, U.z);
+                else
+                  tma_store(&M.out, stage + h * 2048, pw, U.q0 + c + 16 * h, U.z);
+                bulk_commit();
+              }
+            }
           }
         }
       } else {
@@ -668,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const int q0 = a ? U.n[0] : 0, nq = a ? U.nq - U.n[0] : min(U.nq, U.n[0]);
           for (int c = 32 * half; c < nq; c += 64) {
-            if (elect_one()) bulk_wait_read();  // the staging block's last copy has left it
+            if (elect_one()) bulk_wait_read<0>();  // the staging block's last copy has left it
             __syncwarp();
             stage_block<O>(t_lane + 256 * buf + c, U.blocks == 0, stage, lane);
             const int row = U.q0 + q0 + c;
@@ -677,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               fence_async_shared();
               __syncwarp();
               if (pw < P.np && elect_one()) {
-                tma_store_3d(&tmO, stage, pw, row, kMode == kGrad ? U.z : 0);
+                tma_store(&M.out, stage, pw, row, kMode == kGrad ? U.z : 0);
                 bulk_commit();
               }
             } else {
@@ -699,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (!kF32 && elect_one()) bulk_wait();
+    if (elect_one()) bulk_wait();
   }
 
   tc_fence_before();
@@ -728,20 +766,33 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 16-bit tensor [mats][rows][cols] (cols contiguous), boxes of box_rows x box_cols, the
-// rows of a box (128 or 64 bytes) swizzled.
+// Tensor [mats][rows][cols] (cols contiguous) of 2- or 4-byte values, boxes of box_rows x
+// box_cols (of `blocks` column blocks where the columns are split into blocks of 64), the
+// rows of a box swizzled by their length (128, 64 bytes), or not at all.
 bool make_map(CUtensorMap *m, const void *base, uint64_t mats, uint64_t rows, uint64_t cols,
-              uint32_t box_rows, uint32_t box_cols = BT) {
+              uint32_t box_rows, uint32_t box_cols, bool f32, uint32_t blocks = 0) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[3] = {cols, rows, mats};
-  cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
-  cuuint32_t box[3] = {box_cols, box_rows, 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE,
-            box_cols == BT ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+  const uint64_t size = f32 ? 4 : 2;
+  cuuint64_t dims[4] = {blocks ? BT : cols, rows, blocks ? cols / BT : 1, mats};
+  cuuint64_t strides[3] = {cols * size, BT * size, rows * cols * size};
+  cuuint32_t box[4] = {box_cols, box_rows, blocks ? blocks : 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4,
+            const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            f32              ? CU_TENSOR_MAP_SWIZZLE_NONE
+            : box_cols == BT ? CU_TENSOR_MAP_SWIZZLE_128B
+                             : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// K-major operand: boxes of 64 columns.  MN-major: 64 rows of `blocks` column blocks.
+bool map_k_major(CUtensorMap *m, const void *base, uint64_t mats, uint64_t rows, uint64_t cols,
+                 uint32_t box_rows) {
+  return make_map(m, base, mats, rows, cols, box_rows, BT, false);
+}
+bool map_mn_major(CUtensorMap *m, const void *base, uint64_t mats, uint64_t rows, uint64_t cols,
+                  uint32_t blocks) {
+  return make_map(m, base, mats, rows, cols, BT, BT, false, cols % BT == 0 ? blocks : 0);
 }
 
 int check_common(const moe_segments &seg, int n, int k, int type) {
@@ -758,8 +809,7 @@ bool off16(const void *p) { return (uintptr_t)p % 16 != 0; }
 
 // max_units: no more units than this (the grid need not be larger).
 template <int kMode, class O>
-int launch(const CUtensorMap &mp, const CUtensorMap &mq, const CUtensorMap &mo,
-           const GroupedParams &P, int64_t max_units, int num_sms, void *stream) {
+int launch(const Maps &maps, const GroupedParams &P, int64_t max_units, int num_sms, void *stream) {
   static int max_clusters[kMaxDevices] = {};
   const int dev = device_slot();
   if (dev < 0) return dev;
@@ -768,7 +818,8 @@ int launch(const CUtensorMap &mp, const CUtensorMap &mq, const CUtensorMap &mo,
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(sms / 2 > 0 ? sms / 2 * 2 : 2));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  constexpr uint32_t kSmem = smem_bytes(sizeof(O) == 4);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = as_stream(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -779,7 +830,7 @@ int launch(const CUtensorMap &mp, const CUtensorMap &mq, const CUtensorMap &mo,
   cfg.numAttrs = 1;
   if (max_clusters[dev] == 0) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kSmemBytes);
+                                         (int)kSmem);
     int n = 0;
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
     if (e != cudaSuccess || n <= 0)
@@ -791,7 +842,7 @@ int launch(const CUtensorMap &mp, const CUtensorMap &mq, const CUtensorMap &mo,
   if (clusters > max_units) clusters = max_units;
   if (clusters < 1) return MOE_OK;
   cfg.gridDim = dim3((unsigned)(2 * clusters));
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, mp, mq, mo, P);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, maps, P);
   if (e != cudaSuccess) return set_cuda_error(e);
   return check_launch();
 }
@@ -814,21 +865,23 @@ extern "C" int moe_grouped_gemm(const moe_ggemm_args *a, void *stream) {
   P.nt = a->trans ? a->n : a->k;
   P.bf16 = a->type == MOE_TYPE_BF16;
   P.out = a->out;
-  CUtensorMap mp, mq, mo;
-  if (!make_map(&mp, a->w, (uint64_t)a->seg.E, (uint64_t)a->n, (uint64_t)a->k, a->trans ? BT : 128) ||
-      !make_map(&mq, a->x, 1, (uint64_t)a->seg.rows, (uint64_t)P.nt, kBoxRows) ||
-      !make_map(&mo, a->out, 1, (uint64_t)a->seg.rows, (uint64_t)P.np, 32, 32))
-    return MOE_ERR_CUDA;
+  P.p_blocked = a->k % BT == 0;
+  Maps maps = {};
+  const uint64_t E = a->seg.E, n = a->n, k = a->k, rows = a->seg.rows;
+  bool ok = a->trans ? map_mn_major(&maps.p, a->w, E, n, k, 2) : map_k_major(&maps.p, a->w, E, n, k, 128);
+  for (int i = 0; i < 8; ++i) ok = ok && map_k_major(&maps.q[i], a->x, 1, rows, P.nt, 16 * (i + 1));
+  ok = ok && make_map(&maps.out, a->out, 1, rows, P.np, 32, 32, false);
+  if (!ok) return MOE_ERR_CUDA;
   // row tiles: a full one per 512 rows, and one started in every segment that has rows
   const int64_t started = a->seg.E < a->seg.rows ? a->seg.E : a->seg.rows;
   const int64_t max_units = (a->seg.rows / kWide + started) * ((P.np + BP - 1) / BP);
   if (max_units > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   const bool bf = P.bf16;
   if (a->trans)
-    return bf ? launch<kTrans, __nv_bfloat16>(mp, mq, mo, P, max_units, a->num_sms, stream)
-              : launch<kTrans, __half>(mp, mq, mo, P, max_units, a->num_sms, stream);
-  return bf ? launch<kFwd, __nv_bfloat16>(mp, mq, mo, P, max_units, a->num_sms, stream)
-            : launch<kFwd, __half>(mp, mq, mo, P, max_units, a->num_sms, stream);
+    return bf ? launch<kTrans, __nv_bfloat16>(maps, P, max_units, a->num_sms, stream)
+              : launch<kTrans, __half>(maps, P, max_units, a->num_sms, stream);
+  return bf ? launch<kFwd, __nv_bfloat16>(maps, P, max_units, a->num_sms, stream)
+            : launch<kFwd, __half>(maps, P, max_units, a->num_sms, stream);
 }
 
 extern "C" int moe_grouped_wgrad(const moe_wgrad_args *a, void *stream) {
@@ -847,18 +900,21 @@ extern "C" int moe_grouped_wgrad(const moe_wgrad_args *a, void *stream) {
   P.bf16 = a->type == MOE_TYPE_BF16;
   P.out = a->out;
   P.accumulate = a->accumulate != 0;
+  P.p_blocked = a->k % BT == 0;
+  P.q_blocked = a->n % BT == 0;
   // without rows every segment is empty: the maps are not used, and need only be valid
-  const uint64_t rows = a->seg.rows > 0 ? (uint64_t)a->seg.rows : 1;
-  CUtensorMap mp, mq, mo;
-  if (!make_map(&mp, a->seg.rows > 0 ? a->x : a->out, 1, rows, (uint64_t)a->k, BT) ||
-      !make_map(&mq, a->seg.rows > 0 ? a->dy : a->out, 1, rows, (uint64_t)a->n, BT) ||
-      !make_map(&mo, a->out, (uint64_t)a->seg.E, (uint64_t)a->n, (uint64_t)a->k, 32, 32))
-    return MOE_ERR_CUDA;
+  const bool f32 = a->out_type == MOE_TYPE_F32, none = a->seg.rows == 0;
+  const uint64_t E = a->seg.E, n = a->n, k = a->k, rows = none ? 1 : a->seg.rows;
+  Maps maps = {};
+  bool ok = map_mn_major(&maps.p, none ? a->out : a->x, 1, rows, k, 2);
+  for (int i = 0; i < 2; ++i) ok = ok && map_mn_major(&maps.q[i], none ? a->out : a->dy, 1, rows, n, i + 1);
+  ok = ok && make_map(&maps.out, a->out, E, n, k, f32 ? 16 : 32, 32, f32);
+  if (!ok) return MOE_ERR_CUDA;
   const int64_t max_units =
       (int64_t)a->seg.E * ((a->k + BP - 1) / BP) * ((a->n + BQ - 1) / BQ);
   if (max_units > INT32_MAX) return MOE_ERR_UNSUPPORTED;
-  if (a->out_type == MOE_TYPE_F32)
-    return launch<kGrad, float>(mp, mq, mo, P, max_units, a->num_sms, stream);
-  return P.bf16 ? launch<kGrad, __nv_bfloat16>(mp, mq, mo, P, max_units, a->num_sms, stream)
-                : launch<kGrad, __half>(mp, mq, mo, P, max_units, a->num_sms, stream);
+  if (f32)
+    return launch<kGrad, float>(maps, P, max_units, a->num_sms, stream);
+  return P.bf16 ? launch<kGrad, __nv_bfloat16>(maps, P, max_units, a->num_sms, stream)
+                : launch<kGrad, __half>(maps, P, max_units, a->num_sms, stream);
 }
