@@ -44,12 +44,11 @@ constexpr int kThreads = 384, kEpiWarps = 8;
 constexpr int BP = 256, BQ = 256, BT = 64;  // tile of a CTA pair, depth of a block of t
 constexpr int kWide = 2 * BQ;               // q's of a wide unit
 constexpr int kUnitQ = 8;
-constexpr uint32_t kSlotBytes = 128 * BT * 2;  // a CTA's half of a P or Q tile
-// Slots of the operand ring, and an epilogue warp's staging: a 32 x 32 block of 16-bit
+constexpr uint32_t kPBytes = 128 * BT * 2;  // a CTA's half of a P tile
+// Bytes of the operand ring, and an epilogue warp's staging: a 32 x 32 block of 16-bit
 // values, or two 16 x 32 blocks of binary32 ones.
-constexpr int slots_of(bool f32) { return f32 ? 10 : 12; }
+constexpr uint32_t ring_bytes(bool f32) { return (f32 ? 160 : 192) * 1024; }
 constexpr uint32_t stage_bytes(bool f32) { return f32 ? 2 * 2048 : 2048; }
-constexpr int kMaxDepth = 6;  // blocks in the ring: half the slots
 constexpr int kSumBlocks = 8;  // blocks of one partial sum (binary32 output): 512 rows
 constexpr int kWideRows = 1024;  // rows from which the gradient takes wide units
 constexpr uint32_t kTmemCols = 512;
@@ -68,21 +67,29 @@ struct Unit {
   int end;
 };
 
-// The operand ring: block i of the CTA's stream takes two or three consecutive slots (P,
-// and a Q for each accumulator) and the barriers i % kDepth.  Every role that follows the
-// stream keeps such a place.
-template <int kSlots>
+// The operand ring.  Block i of the CTA's stream takes the barriers i % kDepth and, one
+// after the other, room for its P tile and the Q tile of each accumulator, no more than
+// they need: the fewer rows, the more blocks (and bytes of weights) are in flight.  A tile
+// that does not fit before the end starts at 0.  Every role that follows the stream keeps
+// such a place and finds the same one.
+constexpr int kDepth = 10;
+template <uint32_t kBytes>
 struct Ring {
-  int slot = 0, bar = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ uint32_t at(int a) const {  // byte offset of the block's slot a
-    const int s = slot + a;
-    return (uint32_t)(s >= kSlots ? s - kSlots : s) * kSlotBytes;
+  uint32_t pos = 0, phase = 0;
+  int bar = 0;
+  // Where the next tile of `bytes` goes; `used` grows by what it takes, a skipped end too.
+  __device__ __forceinline__ uint32_t place(uint32_t bytes, uint32_t &used) {
+    if (pos + bytes > kBytes) {
+      used += kBytes - pos;
+      pos = 0;
+    }
+    const uint32_t at = pos;
+    used += bytes;
+    pos += bytes;
+    return at;
   }
-  __device__ __forceinline__ void next(int width) {
-    slot += width;
-    if (slot >= kSlots) slot -= kSlots;
-    if (++bar == kSlots / 2) {
+  __device__ __forceinline__ void next_block() {
+    if (++bar == kDepth) {
       bar = 0;
       phase ^= 1;
     }
@@ -90,7 +97,7 @@ struct Ring {
 };
 
 struct Shared {
-  uint64_t full[kMaxDepth], empty[kMaxDepth], tail[kMaxDepth], peer[kMaxDepth];
+  uint64_t full[kDepth], empty[kDepth], tail[kDepth], peer[kDepth];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t unit_full[kUnitQ], unit_empty[kUnitQ];
   Unit unit[kUnitQ];
@@ -99,7 +106,7 @@ struct Shared {
   long long part[33];
   SegTable table;
 };
-constexpr uint32_t off_stage(bool f32) { return slots_of(f32) * kSlotBytes; }
+constexpr uint32_t off_stage(bool f32) { return ring_bytes(f32); }
 constexpr uint32_t off_shared(bool f32) { return off_stage(f32) + kEpiWarps * stage_bytes(f32); }
 constexpr uint32_t smem_bytes(bool f32) { return off_shared(f32) + sizeof(Shared) + 1024; }
 static_assert(smem_bytes(false) <= 232448 && smem_bytes(true) <= 232448, "shared memory");
@@ -330,14 +337,14 @@ template <int kMode, class O>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_kernel(const __grid_constant__ Maps M, const GroupedParams P) {
   constexpr bool kF32 = sizeof(O) == 4;
-  constexpr int kSlots = slots_of(kF32);
+  constexpr uint32_t kRing = ring_bytes(kF32);
   constexpr bool kPMn = kMode != kFwd, kQMn = kMode == kGrad;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Shared &S = *reinterpret_cast<Shared *>(smem + off_shared(kF32));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t s_slots = smem_u32(smem);
+  const uint32_t s_ring = smem_u32(smem);
   const uint32_t bar_full = smem_u32(S.full), bar_empty = smem_u32(S.empty);
   const uint32_t bar_tail = smem_u32(S.tail), bar_peer = smem_u32(S.peer);
   const uint32_t bar_acc_full = smem_u32(S.acc_full), bar_acc_empty = smem_u32(S.acc_empty);
@@ -347,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rank = (int)cluster_ctarank();
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kMaxDepth; ++s) {
+    for (int s = 0; s < kDepth; ++s) {
       mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
       mbar_init(bar_tail + 8 * s, 1);
@@ -430,9 +437,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- producer
       const uint64_t pol_stream = policy_evict_first(), pol_keep = policy_evict_normal();
       const uint32_t lead_full = mapa_shared(bar_full, 0);
-      Ring<kSlots> ring, oldest;  // the block to fill, and the oldest not known to be free
-      int free = kSlots, blocks = 0;
-      uint32_t wide = 0;          // bit i: block i after the oldest takes three slots
+      Ring<kRing> ring, oldest;  // the block to fill, and the oldest not known to be free
+      uint32_t free = kRing;
+      int blocks = 0;            // between them,
+      uint64_t sizes = 0;        // and what each takes: 6 bits, KB, the oldest lowest
       bool ok = true;
       for (int seq = 0; ok; ++seq) {
         Unit U;
@@ -440,26 +448,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         release_unit(seq);
         if (U.end) break;
         const uint64_t pol_p = U.once ? pol_stream : pol_keep;
-        const int p0 = U.p0 + 128 * rank, width = U.n[1] ? 3 : 2;
+        const int p0 = U.p0 + 128 * rank, accs = U.n[1] ? 2 : 1;
         int half[2], q0[2];
         for (int a = 0; a < 2; ++a) {
           half[a] = U.n[a] / 2;
           q0[a] = U.q0 + (a ? U.n[0] : 0) + half[a] * rank;
         }
-        const uint32_t bytes = kSlotBytes + (half[0] + half[1]) * (BT * 2);  // of this CTA
+        const uint32_t bytes = kPBytes + (half[0] + half[1]) * (BT * 2);  // of this CTA
         for (int b = 0; b < U.blocks; ++b) {
-          while (ok && (free < width || blocks == kSlots / 2)) {
+          uint32_t used = 0;
+          const uint32_t dp = s_ring + ring.place(kPBytes, used);
+          uint32_t dq[2];
+          for (int a = 0; a < 2; ++a) dq[a] = a < accs ? s_ring + ring.place(half[a] * (BT * 2), used) : 0;
+          while (ok && (free < used || blocks == kDepth)) {
             ok = wait(bar_empty + 8 * oldest.bar, oldest.phase, kWaitLimitNs);
-            free += 2 + (wide & 1);
-            wide >>= 1;
+            free += (uint32_t)(sizes & 63) * 1024;
+            sizes >>= 6;
             --blocks;
-            oldest.next(0);
+            oldest.next_block();
           }
           if (!ok) break;
           const int t = U.t0 + b * BT;
           auto load = [&](auto pair, uint32_t bar) {
             constexpr bool kPair = decltype(pair)::value;
-            const uint32_t dp = s_slots + ring.at(0);
             if constexpr (kMode == kFwd) {
               tma_load<kPair>(dp, &M.p, bar, t, p0, 0, U.z, pol_p);
             } else if (P.p_blocked) {
@@ -469,15 +480,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load<kPair>(dp + 8192 * j, &M.p, bar, p0 + 64 * j, t, 0,
                                 kMode == kGrad ? 0 : U.z, pol_p);
             }
-            for (int a = 0; a < width - 1; ++a) {
-              const uint32_t dq = s_slots + ring.at(1 + a);
+            for (int a = 0; a < accs; ++a) {
               if constexpr (!kQMn) {
-                tma_load<kPair>(dq, &M.q[half[a] / 16 - 1], bar, t, q0[a], 0, 0, pol_keep);
+                tma_load<kPair>(dq[a], &M.q[half[a] / 16 - 1], bar, t, q0[a], 0, 0, pol_keep);
               } else if (P.q_blocked) {
-                tma_load<kPair>(dq, &M.q[half[a] / 64 - 1], bar, 0, t, q0[a] >> 6, 0, pol_keep);
+                tma_load<kPair>(dq[a], &M.q[half[a] / 64 - 1], bar, 0, t, q0[a] >> 6, 0, pol_keep);
               } else {
                 for (int j = 0; j < half[a] / 64; ++j)
-                  tma_load<kPair>(dq + 8192 * j, &M.q[0], bar, q0[a] + 64 * j, t, 0, 0, pol_keep);
+                  tma_load<kPair>(dq[a] + 8192 * j, &M.q[0], bar, q0[a] + 64 * j, t, 0, 0, pol_keep);
               }
             }
           };
@@ -489,10 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * ring.bar, 2 * bytes);
             load(std::true_type{}, lead_full + 8 * ring.bar);
           }
-          free -= width;
-          wide |= (uint32_t)(width - 2) << blocks;
+          free -= used;
+          sizes |= (uint64_t)(used / 1024) << (6 * blocks);
           ++blocks;
-          ring.next(width);
+          ring.next_block();
         }
       }
       if (*abort) {  // let the copies in flight land before the CTA can exit
@@ -509,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                               ((kPMn ? 1u : 0u) << 15) | ((kQMn ? 1u : 0u) << 16) |
                               ((uint32_t)(BP >> 4) << 24);
       int acc = 0;
-      Ring<kSlots> ring;
+      Ring<kRing> ring;
       bool ok = true;
       for (int seq = 0; ok; ++seq) {
         Unit U;
@@ -530,10 +540,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait(bar_full + 8 * ring.bar, ring.phase, kWaitLimitNs);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t sp = s_slots + ring.at(0);
+            uint32_t used = 0;
+            const uint32_t sp = s_ring + ring.place(kPBytes, used);
             const int steps = b == U.blocks - 1 ? (U.rem + 15) >> 4 : BT / 16;
             for (int a = 0; a < accs; ++a) {
-              const uint32_t sq = s_slots + ring.at(1 + a);
+              const uint32_t sq = s_ring + ring.place(U.n[a] / 2 * (BT * 2), used);
               const uint32_t d = tmem + 256 * ((acc + a) & 1);
               const uint32_t idesc = idesc0 | ((uint32_t)(U.n[a] >> 3) << 17);
 #pragma unroll
@@ -543,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                (b != b0) | (j != 0));
             }
             tc_commit_pair_mc(bar_empty + 8 * ring.bar, kBoth);
-            ring.next(1 + accs);
+            ring.next_block();
           }
           if (!ok) break;
           for (int a = 0; a < accs; ++a) tc_commit_pair_mc(bar_acc_full + 8 * ((acc + a) & 1), kBoth);
@@ -573,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (kMode == kGrad && warp == 3) {
       // -------------------------------------- rows past the segment's last
       const uint32_t lead_peer = mapa_shared(bar_peer, 0);
-      int64_t slot = 0, block = 0;
+      Ring<kRing> ring;
       uint32_t parity = 0;  // of each tail and peer barrier
       for (int seq = 0;; ++seq) {
         Unit U;
@@ -581,20 +592,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) release_unit(seq);
         if (U.end) break;
-        const int width = U.n[1] ? 3 : 2;
-        slot += (int64_t)U.blocks * width;  // after the unit
-        block += U.blocks;
+        const int accs = U.n[1] ? 2 : 1;
+        uint32_t at[3], bytes[3] = {kPBytes, U.n[0] * (uint32_t)BT, U.n[1] * (uint32_t)BT}, used = 0;
+        int bar = 0;
+        for (int b = 0; b < U.blocks; ++b) {
+          for (int a = 0; a <= 2; ++a)
+            if (a <= accs) at[a] = ring.place(bytes[a], used);
+          bar = ring.bar;
+          ring.next_block();
+        }
         if (U.blocks == 0 || (U.rem & 15) == 0) continue;
-        const int bar = (int)((block - 1) % (kSlots / 2));
         if (!wait_warp(bar_tail + 8 * bar, (parity >> bar) & 1u, unit_limit)) break;
-        // 8 pieces of 16 bytes a row, in the two column blocks of each slot
+        // 8 pieces of 16 bytes a row, in each tile's one or two column blocks
         const int lines = 16 - (U.rem & 15);
-        for (int a = 0; a < width; ++a) {
-          uint8_t *base = smem + (slot - width + a) % kSlots * kSlotBytes;
-          for (int i = lane; i < lines * 16; i += 32) {
-            const int row = U.rem + (i >> 4), half = (i >> 3) & 1, piece = i & 7;
-            *reinterpret_cast<uint4 *>(base + half * 8192 + row * 128 + piece * 16) =
-                make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int a = 0; a <= 2; ++a) {
+          if (a > accs) break;
+          for (int i = lane; i < lines * 8 * (int)(bytes[a] / 8192); i += 32) {
+            const int piece = i & 7, line = (i >> 3) % lines, block = (i >> 3) / lines;
+            *reinterpret_cast<uint4 *>(smem + at[a] + block * 8192 + (U.rem + line) * 128 +
+                                       piece * 16) = make_uint4(0, 0, 0, 0);
           }
         }
         fence_async_shared();
