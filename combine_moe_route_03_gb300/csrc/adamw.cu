@@ -87,30 +87,34 @@ __device__ __forceinline__ void store_copy4(void *c, int type, int64_t i, const 
 }
 
 // Codes: see moe_adamw in include/moe.h.
-__device__ __forceinline__ float decode_m(int c, float s) {
-  const float q = __fmul_rn((float)c, kInvM);
+// Byte k of w as a float, exactly: as the low bits of 2^23 + byte.
+__device__ __forceinline__ float byte_f32(uint32_t w, int k) {
+  return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 | k)) - 8388608.0f;
+}
+// Code k of a word of four.  m: the sign bits flipped (w ^ 0x80808080) make a byte of c + 128.
+__device__ __forceinline__ float decode_m(uint32_t flipped, int k, float s) {
+  const float q = __fmul_rn(byte_f32(flipped, k) - 128.0f, kInvM);
   return __fmul_rn(__fmul_rn(q, fabsf(q)), s);
 }
-__device__ __forceinline__ float decode_r(int c, float s) {
-  const float q = __fmul_rn((float)c, kInvR);
+__device__ __forceinline__ float decode_r(uint32_t w, int k, float s) {
+  const float q = __fmul_rn(byte_f32(w, k), kInvR);
   return __fmul_rn(__fmul_rn(q, q), s);
 }
-// The whole number c with (c - 1/2)^2 <= z < (c + 1/2)^2, z = levels^2 x / s: a square
-// root of any rounding is within one of it, and the two bounds (exact in binary32) say
-// which way.
-__device__ __forceinline__ int square_code(float x, float inv, float sq, int levels) {
+// The whole number c with (c - 1/2)^2 <= z < (c + 1/2)^2, z = levels^2 x / s.  An
+// approximate root, pulled down by more than its error and rounded to the nearest whole
+// number, is c or c - 1; the bound between them, exact in binary32, says which.  Adding
+// 1.5 * 2^23 rounds, and leaves the number in the low bits.
+__device__ __forceinline__ uint32_t square_code(float x, float inv, float sq) {
+  constexpr float kRound = 12582912.0f;
   const float z = __fmul_rn(__fmul_rn(x, inv), sq);
   float root;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(z));
-  const float c = rintf(root);
-  const float lo = c - 0.5f, hi = c + 0.5f;
-  int k = (int)c;  // NaN: 0
-  k -= (z < lo * lo && c > 0.0f) ? 1 : 0;
-  k += z >= hi * hi ? 1 : 0;
-  return min(k, levels);
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(z));  // a subnormal z is code 0 either way
+  const float y = __fmaf_rn(root, 1.0f - 0x1p-20f, kRound);
+  const float h = __fadd_rn(__fadd_rn(y, -kRound), 0.5f);
+  return (__float_as_uint(y) & 0xffu) + (z >= __fmul_rn(h, h) ? 1u : 0u);
 }
 __device__ __forceinline__ float block_inverse(float s) {
-  return s >= 1.17549435e-38f ? __fdiv_rn(1.0f, s) : (s != s ? s : 0.0f);
+  return s >= 1.17549435e-38f ? __fdiv_rn(1.0f, s) : 0.0f;
 }
 // Largest magnitude of the warp's block; a NaN wins over every number.
 __device__ __forceinline__ float block_max(const float *x) {
@@ -119,6 +123,7 @@ __device__ __forceinline__ float block_max(const float *x) {
   for (int j = 0; j < 8; ++j) b = max(b, __float_as_uint(x[j]) & 0x7fffffffu);
   return __uint_as_float(__reduce_max_sync(0xffffffffu, b));
 }
+__device__ __forceinline__ bool finite(float s) { return s <= 3.402823466e+38f; }
 
 // Value j (0..7) of this lane sits at this place of its block.
 __device__ __forceinline__ int place(int lane, int j) { return 128 * (j >> 2) + 4 * lane + (j & 3); }
@@ -152,42 +157,54 @@ __device__ __forceinline__ void store_f32(float *p, bool fast, int lane, int64_t
     each(lane, n, [&](int j, int i) { p[i] = o[j]; });
   }
 }
-__device__ __forceinline__ void load_codes(const uint8_t *p, bool fast, int lane, int64_t n, uint8_t *o) {
+// Codes of one lane, four to a word: w[0] its values of the block's first half.
+__device__ __forceinline__ void load_codes(const uint8_t *p, bool fast, int lane, int64_t n, uint32_t *w) {
   if (fast) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<uint32_t *>(o + 4 * h) =
-          __ldcs(reinterpret_cast<const uint32_t *>(p + place(lane, 4 * h)));
+    for (int h = 0; h < 2; ++h) w[h] = __ldcs(reinterpret_cast<const uint32_t *>(p + place(lane, 4 * h)));
   } else {
-    each(lane, n, [&](int j, int i) { o[j] = p[i]; });
+    w[0] = w[1] = 0;
+    each(lane, n, [&](int j, int i) { w[j >> 2] |= (uint32_t)p[i] << (8 * (j & 3)); });
   }
 }
-__device__ __forceinline__ void store_codes(uint8_t *p, bool fast, int lane, int64_t n, const uint8_t *o) {
+__device__ __forceinline__ void store_codes(uint8_t *p, bool fast, int lane, int64_t n, const uint32_t *w) {
   if (fast) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      __stcs(reinterpret_cast<uint32_t *>(p + place(lane, 4 * h)),
-             *reinterpret_cast<const uint32_t *>(o + 4 * h));
+    for (int h = 0; h < 2; ++h) __stcs(reinterpret_cast<uint32_t *>(p + place(lane, 4 * h)), w[h]);
   } else {
-    each(lane, n, [&](int j, int i) { p[i] = o[j]; });
+    each(lane, n, [&](int j, int i) { p[i] = (uint8_t)(w[j >> 2] >> (8 * (j & 3))); });
   }
 }
-struct alignas(8) Codes {
-  uint8_t c[8];
-};
-
-// New moments of a block -> codes and scales.
-__device__ __forceinline__ void encode_block(const float *m, const float *r, Codes &mc, Codes &rc,
+__device__ __forceinline__ void decode_block(const uint32_t *mc, const uint32_t *rc, float ms, float rs,
+                                             float *m, float *v) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    m[j] = decode_m(mc[j >> 2] ^ 0x80808080u, j & 3, ms);
+    const float x = decode_r(rc[j >> 2], j & 3, rs);
+    v[j] = __fmul_rn(x, x);
+  }
+}
+// Moments of a block (r = sqrt(v)) -> codes and scales.
+__device__ __forceinline__ void encode_block(const float *m, const float *r, uint32_t *mc, uint32_t *rc,
                                              float &ms, float &rs) {
   ms = block_max(m);
   rs = block_max(r);
-  const float mi = block_inverse(ms), ri = block_inverse(rs);
+  mc[0] = mc[1] = rc[0] = rc[1] = 0;
+  if (finite(ms)) {  // else: code 0, which an infinite or NaN scale turns into NaN
+    const float inv = block_inverse(ms);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t c = square_code(fabsf(m[j]), inv, kSqM);
+      mc[j >> 2] |= ((m[j] < 0.0f ? 0u - c : c) & 0xffu) << (8 * (j & 3));
+    }
+  }
+  const float inv = finite(rs) ? block_inverse(rs) : 0.0f;
+  const bool ok = finite(rs);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int c = square_code(fabsf(m[j]), mi, kSqM, 127);
-    mc.c[j] = (uint8_t)(int8_t)(m[j] < 0.0f ? -c : c);
-    const int d = square_code(r[j], ri, kSqR, 255);
-    rc.c[j] = (uint8_t)(r[j] > 0.0f ? max(d, 1) : d);
+    uint32_t d = ok ? square_code(r[j], inv, kSqR) : 0u;
+    if (r[j] > 0.0f) d = max(d, 1u);
+    rc[j >> 2] |= d << (8 * (j & 3));
   }
 }
 
@@ -222,16 +239,10 @@ __global__ void __launch_bounds__(kThreads)
       each(lane, n, [&](int j, int i) { g[j] = load_g(T.g, T.g_type, i0 + i); });
     }
     if constexpr (k8Bit) {
-      Codes mc = {}, rc = {};
-      load_codes(static_cast<const uint8_t *>(T.m) + i0, fast, lane, n, mc.c);
-      load_codes(static_cast<const uint8_t *>(T.v) + i0, fast, lane, n, rc.c);
-      const float ms = T.m_scale[b], rs = T.r_scale[b];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m[j] = decode_m((int8_t)mc.c[j], ms);
-        const float x = decode_r(rc.c[j], rs);
-        v[j] = __fmul_rn(x, x);
-      }
+      uint32_t mc[2], rc[2];
+      load_codes(static_cast<const uint8_t *>(T.m) + i0, fast, lane, n, mc);
+      load_codes(static_cast<const uint8_t *>(T.v) + i0, fast, lane, n, rc);
+      decode_block(mc, rc, T.m_scale[b], T.r_scale[b], m, v);
     } else {
       load_f32(static_cast<const float *>(T.m) + i0, fast, lane, n, m);
       load_f32(static_cast<const float *>(T.v) + i0, fast, lane, n, v);
@@ -243,7 +254,7 @@ __global__ void __launch_bounds__(kThreads)
       v[j] = __fadd_rn(__fmul_rn(v[j], H.beta2), __fmul_rn(__fmul_rn(x, x), H.alpha2));
       r[j] = __fsqrt_rn(v[j]);
       const float denom = fmaf(r[j], H.inv_bc2, H.eps);
-      p[j] = __fadd_rn(__fmul_rn(p[j], H.decay), -__fmul_rn(__fdiv_rn(m[j], denom), H.step));
+      p[j] = fmaf(p[j], H.decay, -__fdividef(m[j], denom) * H.step);
     }
     store_f32(T.p + i0, fast, lane, n, p);
     if (T.copy) {
@@ -260,11 +271,11 @@ __global__ void __launch_bounds__(kThreads)
         for (int j = 0; j < 8; ++j)
           if (place(lane, j) >= n) m[j] = r[j] = 0.0f;
       }
-      Codes mc, rc;
+      uint32_t mc[2], rc[2];
       float ms, rs;
       encode_block(m, r, mc, rc, ms, rs);
-      store_codes(static_cast<uint8_t *>(T.m) + i0, fast, lane, n, mc.c);
-      store_codes(static_cast<uint8_t *>(T.v) + i0, fast, lane, n, rc.c);
+      store_codes(static_cast<uint8_t *>(T.m) + i0, fast, lane, n, mc);
+      store_codes(static_cast<uint8_t *>(T.v) + i0, fast, lane, n, rc);
       if (lane == 0) {
         T.m_scale[b] = ms;
         T.r_scale[b] = rs;
@@ -286,7 +297,7 @@ __global__ void __launch_bounds__(kThreads)
     const int64_t i0 = b * kBlock, n = n_all - i0;
     const bool fast = n >= kBlock;
     float m[8] = {}, v[8] = {};
-    Codes mc = {}, rc = {};
+    uint32_t mc[2], rc[2];
     if constexpr (kEncode) {
       load_f32(mp + i0, fast, lane, n, m);
       load_f32(vp + i0, fast, lane, n, v);
@@ -294,22 +305,16 @@ __global__ void __launch_bounds__(kThreads)
       for (int j = 0; j < 8; ++j) v[j] = __fsqrt_rn(v[j]);
       float ms, rs;
       encode_block(m, v, mc, rc, ms, rs);
-      store_codes(m_code + i0, fast, lane, n, mc.c);
-      store_codes(r_code + i0, fast, lane, n, rc.c);
+      store_codes(m_code + i0, fast, lane, n, mc);
+      store_codes(r_code + i0, fast, lane, n, rc);
       if (lane == 0) {
         m_scale[b] = ms;
         r_scale[b] = rs;
       }
     } else {
-      load_codes(m_code + i0, fast, lane, n, mc.c);
-      load_codes(r_code + i0, fast, lane, n, rc.c);
-      const float ms = m_scale[b], rs = r_scale[b];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m[j] = decode_m((int8_t)mc.c[j], ms);
-        const float x = decode_r(rc.c[j], rs);
-        v[j] = __fmul_rn(x, x);
-      }
+      load_codes(m_code + i0, fast, lane, n, mc);
+      load_codes(r_code + i0, fast, lane, n, rc);
+      decode_block(mc, rc, m_scale[b], r_scale[b], m, v);
       store_f32(mp + i0, fast, lane, n, m);
       store_f32(vp + i0, fast, lane, n, v);
     }

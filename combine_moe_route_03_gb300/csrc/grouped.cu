@@ -45,14 +45,19 @@ constexpr int BP = 256, BQ = 256, BT = 64;  // tile of a CTA pair, depth of a bl
 constexpr int kWide = 2 * BQ;               // q's of a wide unit
 constexpr int kUnitQ = 8;
 constexpr uint32_t kPBytes = 128 * BT * 2;  // a CTA's half of a P tile
-// Bytes of the operand ring, and an epilogue warp's staging: a 32 x 32 block of 16-bit
-// values, or two 16 x 32 blocks of binary32 ones.
+// Bytes of the operand ring, and an epilogue warp's staging: a block of 32 x 32 16-bit
+// values, or two in turn of 16 x 32 binary32 ones.
 constexpr uint32_t ring_bytes(bool f32) { return (f32 ? 160 : 192) * 1024; }
-constexpr uint32_t stage_bytes(bool f32) { return f32 ? 2 * 2048 : 2048; }
+constexpr uint32_t kStage = 2048;
+constexpr uint32_t stage_bytes(bool f32) { return f32 ? 2 * kStage : kStage; }
 constexpr int kSumBlocks = 8;  // blocks of one partial sum (binary32 output): 512 rows
 constexpr int kWideRows = 1024;  // rows from which the gradient takes wide units
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+
+__host__ __device__ constexpr uint32_t block_bytes(int n0, int n1) {  // of one CTA
+  return kPBytes + (uint32_t)(n0 + n1) / 2 * (BT * 2);
+}
 
 struct Unit {
   int z;      // expert
@@ -67,25 +72,26 @@ struct Unit {
   int end;
 };
 
-// The operand ring.  Block i of the CTA's stream takes the barriers i % kDepth and, one
-// after the other, room for its P tile and the Q tile of each accumulator, no more than
-// they need: the fewer rows, the more blocks (and bytes of weights) are in flight.  A tile
-// that does not fit before the end starts at 0.  Every role that follows the stream keeps
-// such a place and finds the same one.
+// The operand ring.  Block i of the CTA's stream takes the barriers i % kDepth and room for
+// its P tile and the Q tile of each accumulator, no more than they need: the fewer rows,
+// the more blocks (and bytes of weights) are in flight.  A block that does not fit before
+// the end starts at 0.  Every role that follows the stream keeps such a place and finds
+// the same one.
 constexpr int kDepth = 10;
 template <uint32_t kBytes>
 struct Ring {
-  uint32_t pos = 0, phase = 0;
+  uint32_t pos = 0, end = 0;  // of the last block: its first byte after; the same, counted through
+  uint32_t phase = 0;
   int bar = 0;
-  // Where the next tile of `bytes` goes; `used` grows by what it takes, a skipped end too.
-  __device__ __forceinline__ uint32_t place(uint32_t bytes, uint32_t &used) {
+  // The place of the next block of `bytes`.
+  __device__ __forceinline__ uint32_t place(uint32_t bytes) {
     if (pos + bytes > kBytes) {
-      used += kBytes - pos;
+      end += kBytes - pos;
       pos = 0;
     }
     const uint32_t at = pos;
-    used += bytes;
     pos += bytes;
+    end += bytes;
     return at;
   }
   __device__ __forceinline__ void next_block() {
@@ -101,6 +107,7 @@ struct Shared {
   uint64_t acc_full[2], acc_empty[2];
   uint64_t unit_full[kUnitQ], unit_empty[kUnitQ];
   Unit unit[kUnitQ];
+  uint32_t end[kDepth];  // Ring::end of the block that each barrier pair serves
   uint32_t tmem;
   int abort;
   long long part[33];
@@ -228,13 +235,15 @@ __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// 16 t's of a stage: K-major rows of 128 bytes (step 32 bytes), or MN-major blocks of 64
-// columns, 128 bytes per t (step 16 t's; column blocks 8 KB apart).
+// Operand descriptors without their address, and what 16 t's add to it: K-major rows of
+// 128 bytes (32 bytes a step), or MN-major blocks of 64 columns, 128 bytes per t (16 t's a
+// step; column blocks 8 KB apart).  Addresses count 16 bytes.
 template <bool kMnMajor>
-__device__ __forceinline__ uint64_t operand_desc(uint32_t base, int step) {
-  return kMnMajor ? smem_desc(base + 2048 * step, BT * 128, 1024, 2)
-                  : smem_desc(base + 32 * step, 16, 1024, 2);
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+  return (kMnMajor ? smem_desc(0, BT * 128, 1024, 2) : smem_desc(0, 16, 1024, 2)) + (addr >> 4);
 }
+template <bool kMnMajor>
+constexpr uint64_t kStep = kMnMajor ? 2048 / 16 : 32 / 16;
 
 // ------------------------------------------------------------------- schedule
 // Rows of a segment's row tiles: one tile of up to 256 (one accumulator, the other one
@@ -266,12 +275,13 @@ __device__ __forceinline__ int grad_q(int nq, int count) {
 }
 
 // Unit u: the segments in order, within one the p tiles, within one the row tiles (or, for
-// the gradient, the q tiles), so units that share a weight tile run side by side.
+// the gradient, the q tiles), so units that share a weight tile run side by side.  e: the
+// segment of the caller's last unit, or -1.
 template <int kMode, bool kF32>
 __device__ __forceinline__ Unit get_unit(const GroupedParams &P, const SegTable &T, int u,
-                                         int p_tiles) {
+                                         int p_tiles, int &e) {
   Unit U = {};
-  const int e = find_segment(T, P.seg.E, u / p_tiles);
+  if (e < 0 || u >= T.before[e + 1] * p_tiles) e = find_segment(T, P.seg.E, u / p_tiles);
   const int tiles = T.before[e + 1] - T.before[e];  // q tiles of the segment
   const int local = u - T.before[e] * p_tiles, qt = local % tiles, count = T.count[e];
   U.z = e;
@@ -307,30 +317,33 @@ __device__ __forceinline__ uint32_t pack2(uint32_t lo, uint32_t hi) {
   return r;
 }
 
-// 32 accumulator columns (q) of this warp's 32 lanes (p) -> 16-bit rows [q][p] of 64 bytes
-// in the warp's staging block, 16-byte pieces swizzled by row (the 64-byte TMA swizzle:
-// neither these writes nor the copies out conflict on banks).
+// 32 accumulator columns (q) of this warp's 32 lanes (p), rounded: w[8h + 2i + (0, 1)] holds
+// lanes 16h + (0, 8) + t/4, columns 8i + 2(t%4) and +1 of thread t.
+__device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t *v) {
+  tmem_ld_16x256b_x4(taddr, v);
+  tmem_ld_16x256b_x4(taddr + (16u << 16), v + 16);
+}
+template <class O>
+__device__ __forceinline__ void round_columns(const uint32_t *v, bool zero, uint32_t *w) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = zero ? 0u : pack2<O>(v[2 * i], v[2 * i + 1]);
+}
+// The block transposed into the warp's staging: rows [q][p] of 64 bytes, 16-byte pieces
+// swizzled by row (the 64-byte TMA swizzle: neither these writes nor the copies out
+// conflict on banks).
 __device__ __forceinline__ uint32_t stage_offset(int q, int piece) {
   return 64 * q + 16 * (piece ^ ((q >> 1) & 3));
 }
-template <class O>
-__device__ __forceinline__ void stage_block(uint32_t taddr, bool zero, uint32_t stage, int lane) {
-  const int m = lane >> 3, j = lane & 7;
+__device__ __forceinline__ void stage_rows(const uint32_t *w, uint32_t stage, int lane) {
+  const int m = lane >> 3;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t v[16];
-    tmem_ld_16x256b_x4(taddr + ((uint32_t)(16 * h) << 16), v);
-    tc_wait_ld();
-    if (zero) {
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0;
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t *x = w + 8 * h + 4 * i;
+      stmatrix_x4_trans(stage + stage_offset(16 * i + 8 * (m >> 1) + (lane & 7), 2 * h + (m & 1)),
+                        x[0], x[1], x[2], x[3]);
     }
-#pragma unroll
-    for (int i = 0; i < 4; i += 2)
-      stmatrix_x4_trans(stage + stage_offset(8 * (i + (m >> 1)) + j, 2 * h + (m & 1)),
-                        pack2<O>(v[4 * i], v[4 * i + 1]), pack2<O>(v[4 * i + 2], v[4 * i + 3]),
-                        pack2<O>(v[4 * i + 4], v[4 * i + 5]), pack2<O>(v[4 * i + 6], v[4 * i + 7]));
-  }
 }
 
 template <int kMode, class O>
@@ -437,61 +450,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- producer
       const uint64_t pol_stream = policy_evict_first(), pol_keep = policy_evict_normal();
       const uint32_t lead_full = mapa_shared(bar_full, 0);
-      Ring<kRing> ring, oldest;  // the block to fill, and the oldest not known to be free
-      uint32_t free = kRing;
-      int blocks = 0;            // between them,
-      uint64_t sizes = 0;        // and what each takes: 6 bits, KB, the oldest lowest
-      bool ok = true;
-      for (int seq = 0; ok; ++seq) {
+      Ring<kRing> ring;
+      uint32_t freed = 0;           // Ring::end of the last block that is known to be consumed,
+      int old_bar = 0, blocks = 0;  // the barriers of the next, and the blocks not known to be
+      uint32_t old_phase = 0;
+      for (int seq = 0;; ++seq) {
         Unit U;
         if (!take(seq, U)) break;
         release_unit(seq);
         if (U.end) break;
         const uint64_t pol_p = U.once ? pol_stream : pol_keep;
-        const int p0 = U.p0 + 128 * rank, accs = U.n[1] ? 2 : 1;
-        int half[2], q0[2];
-        for (int a = 0; a < 2; ++a) {
-          half[a] = U.n[a] / 2;
-          q0[a] = U.q0 + (a ? U.n[0] : 0) + half[a] * rank;
-        }
-        const uint32_t bytes = kPBytes + (half[0] + half[1]) * (BT * 2);  // of this CTA
-        for (int b = 0; b < U.blocks; ++b) {
-          uint32_t used = 0;
-          const uint32_t dp = s_ring + ring.place(kPBytes, used);
-          uint32_t dq[2];
-          for (int a = 0; a < 2; ++a) dq[a] = a < accs ? s_ring + ring.place(half[a] * (BT * 2), used) : 0;
-          while (ok && (free < used || blocks == kDepth)) {
-            ok = wait(bar_empty + 8 * oldest.bar, oldest.phase, kWaitLimitNs);
-            free += (uint32_t)(sizes & 63) * 1024;
-            sizes >>= 6;
+        const int half0 = U.n[0] / 2, half1 = U.n[1] / 2;
+        const int p0 = U.p0 + 128 * rank, qa = U.q0 + half0 * rank, qb = U.q0 + U.n[0] + half1 * rank;
+        constexpr int kUnitN = kQMn ? 64 : 16;
+        const CUtensorMap *map_a = &M.q[half0 / kUnitN - 1], *map_b = &M.q[half1 ? half1 / kUnitN - 1 : 0];
+        const uint32_t bytes = block_bytes(U.n[0], U.n[1]), to_b = kPBytes + half0 * (BT * 2);
+        const int z = kMode == kGrad ? 0 : U.z;
+        const int tail = kMode == kGrad && (U.rem & 15) ? U.blocks - 1 : -1;
+        int t = U.t0;
+        bool ok = true;
+        for (int b = 0; b < U.blocks; ++b, t += BT) {
+          const uint32_t dst = s_ring + ring.place(bytes);
+          while (ring.end - freed > kRing || blocks == kDepth) {
+            ok = wait(bar_empty + 8 * old_bar, old_phase, kWaitLimitNs);
+            if (!ok) break;
+            freed = *(volatile uint32_t *)&S.end[old_bar];
             --blocks;
-            oldest.next_block();
+            if (++old_bar == kDepth) {
+              old_bar = 0;
+              old_phase ^= 1;
+            }
           }
           if (!ok) break;
-          const int t = U.t0 + b * BT;
-          auto load = [&](auto pair, uint32_t bar) {
-            constexpr bool kPair = decltype(pair)::value;
-            if constexpr (kMode == kFwd) {
-              tma_load<kPair>(dp, &M.p, bar, t, p0, 0, U.z, pol_p);
-            } else if (P.p_blocked) {
-              tma_load<kPair>(dp, &M.p, bar, 0, t, p0 >> 6, kMode == kGrad ? 0 : U.z, pol_p);
-            } else {
-              for (int j = 0; j < 2; ++j)
-                tma_load<kPair>(dp + 8192 * j, &M.p, bar, p0 + 64 * j, t, 0,
-                                kMode == kGrad ? 0 : U.z, pol_p);
-            }
-            for (int a = 0; a < accs; ++a) {
+          *(volatile uint32_t *)&S.end[ring.bar] = ring.end;
+          auto load = [&](auto counted_by_pair, uint32_t bar) {
+            constexpr bool kPair = decltype(counted_by_pair)::value;
+            auto tile = [&](uint32_t to, const CUtensorMap *map, int q, int half) {
               if constexpr (!kQMn) {
-                tma_load<kPair>(dq[a], &M.q[half[a] / 16 - 1], bar, t, q0[a], 0, 0, pol_keep);
+                tma_load<kPair>(to, map, bar, t, q, 0, 0, pol_keep);
               } else if (P.q_blocked) {
-                tma_load<kPair>(dq[a], &M.q[half[a] / 64 - 1], bar, 0, t, q0[a] >> 6, 0, pol_keep);
+                tma_load<kPair>(to, map, bar, 0, t, q >> 6, 0, pol_keep);
               } else {
-                for (int j = 0; j < half[a] / 64; ++j)
-                  tma_load<kPair>(dq[a] + 8192 * j, &M.q[0], bar, q0[a] + 64 * j, t, 0, 0, pol_keep);
+                for (int j = 0; j < half; j += 64)
+                  tma_load<kPair>(to + 128 * j, &M.q[0], bar, q + j, t, 0, 0, pol_keep);
               }
+            };
+            if constexpr (kMode == kFwd) {
+              tma_load<kPair>(dst, &M.p, bar, t, p0, 0, z, pol_p);
+            } else if (P.p_blocked) {
+              tma_load<kPair>(dst, &M.p, bar, 0, t, p0 >> 6, z, pol_p);
+            } else {
+              tma_load<kPair>(dst, &M.p, bar, p0, t, 0, z, pol_p);
+              tma_load<kPair>(dst + 8192, &M.p, bar, p0 + 64, t, 0, z, pol_p);
             }
+            tile(dst + kPBytes, map_a, qa, half0);
+            if (half1) tile(dst + to_b, map_b, qb, half1);
           };
-          if (kMode == kGrad && b == U.blocks - 1 && (U.rem & 15)) {
+          if (kMode == kGrad && b == tail) {
             // completes in this CTA, for its tail warp
             mbar_arrive_expect_tx(bar_tail + 8 * ring.bar, bytes);
             load(std::false_type{}, bar_tail + 8 * ring.bar);
@@ -499,11 +514,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * ring.bar, 2 * bytes);
             load(std::true_type{}, lead_full + 8 * ring.bar);
           }
-          free -= used;
-          sizes |= (uint64_t)(used / 1024) << (6 * blocks);
           ++blocks;
           ring.next_block();
         }
+        if (!ok) break;
       }
       if (*abort) {  // let the copies in flight land before the CTA can exit
         const uint64_t t0 = globaltimer();
@@ -528,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (U.end) break;
         if (rank != 0) continue;  // the odd CTA only follows the unit stream
         const int accs = U.n[1] ? 2 : 1, sums = sums_of(U);
+        const uint32_t bytes = block_bytes(U.n[0], U.n[1]);
         for (int s = 0; s < sums && ok; ++s, acc += accs) {
           for (int a = 0; a < accs && ok; ++a)
             ok = wait(bar_acc_empty + 8 * ((acc + a) & 1), ((uint32_t)((acc + a) >> 1) & 1u) ^ 1u,
@@ -540,18 +555,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait(bar_full + 8 * ring.bar, ring.phase, kWaitLimitNs);
             if (!ok) break;
             tc_fence_after();
-            uint32_t used = 0;
-            const uint32_t sp = s_ring + ring.place(kPBytes, used);
+            const uint32_t sp = s_ring + ring.place(bytes);
+            uint32_t sq = sp + kPBytes;
             const int steps = b == U.blocks - 1 ? (U.rem + 15) >> 4 : BT / 16;
             for (int a = 0; a < accs; ++a) {
-              const uint32_t sq = s_ring + ring.place(U.n[a] / 2 * (BT * 2), used);
               const uint32_t d = tmem + 256 * ((acc + a) & 1);
               const uint32_t idesc = idesc0 | ((uint32_t)(U.n[a] >> 3) << 17);
+              const uint64_t dp = operand_desc<kPMn>(sp), dq = operand_desc<kQMn>(sq);
+              mma_pair_f16(d, dp, dq, idesc, b != b0);
+              if (steps == BT / 16) {
 #pragma unroll
-              for (int j = 0; j < BT / 16; ++j)
-                if (j < steps)
-                  mma_pair_f16(d, operand_desc<kPMn>(sp, j), operand_desc<kQMn>(sq, j), idesc,
-                               (b != b0) | (j != 0));
+                for (int j = 1; j < BT / 16; ++j)
+                  mma_pair_f16(d, dp + j * kStep<kPMn>, dq + j * kStep<kQMn>, idesc, 1);
+              } else {
+                for (int j = 1; j < steps; ++j)
+                  mma_pair_f16(d, dp + j * kStep<kPMn>, dq + j * kStep<kQMn>, idesc, 1);
+              }
+              sq += U.n[0] / 2 * (BT * 2);
             }
             tc_commit_pair_mc(bar_empty + 8 * ring.bar, kBoth);
             ring.next_block();
@@ -574,8 +594,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       bool ok = true;
+      int segment = -1;
       for (int u = cluster_id_x(); ok && u < units; u += cluster_count_x())
-        ok = push(get_unit<kMode, kF32>(P, S.table, u, p_tiles));
+        ok = push(get_unit<kMode, kF32>(P, S.table, u, p_tiles, segment));
       if (ok) {
         Unit end = {};
         end.end = 1;
@@ -592,27 +613,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) release_unit(seq);
         if (U.end) break;
-        const int accs = U.n[1] ? 2 : 1;
-        uint32_t at[3], bytes[3] = {kPBytes, U.n[0] * (uint32_t)BT, U.n[1] * (uint32_t)BT}, used = 0;
+        const uint32_t bytes = block_bytes(U.n[0], U.n[1]);
+        uint32_t at = 0;
         int bar = 0;
         for (int b = 0; b < U.blocks; ++b) {
-          for (int a = 0; a <= 2; ++a)
-            if (a <= accs) at[a] = ring.place(bytes[a], used);
+          at = ring.place(bytes);
           bar = ring.bar;
           ring.next_block();
         }
         if (U.blocks == 0 || (U.rem & 15) == 0) continue;
         if (!wait_warp(bar_tail + 8 * bar, (parity >> bar) & 1u, unit_limit)) break;
-        // 8 pieces of 16 bytes a row, in each tile's one or two column blocks
-        const int lines = 16 - (U.rem & 15);
+        // a row: 8 pieces of 16 bytes in each column block of each tile
+        const int first = U.rem + (lane >> 3), last = (U.rem + 15) & ~15;
+        for (uint32_t block = at; block < at + bytes; block += 8192) {
+          uint8_t *base = smem + block + (lane & 7) * 16;
 #pragma unroll
-        for (int a = 0; a <= 2; ++a) {
-          if (a > accs) break;
-          for (int i = lane; i < lines * 8 * (int)(bytes[a] / 8192); i += 32) {
-            const int piece = i & 7, line = (i >> 3) % lines, block = (i >> 3) / lines;
-            *reinterpret_cast<uint4 *>(smem + at[a] + block * 8192 + (U.rem + line) * 128 +
-                                       piece * 16) = make_uint4(0, 0, 0, 0);
-          }
+          for (int i = 0; i < 16; i += 4)
+            if (first + i < last) *reinterpret_cast<uint4 *>(base + (first + i) * 128) = make_uint4(0, 0, 0, 0);
         }
         fence_async_shared();
         __syncwarp();
@@ -638,8 +655,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t t_lane = tmem + ((uint32_t)(32 * quarter) << 16);
     const uint32_t lead_acc_empty = mapa_shared(bar_acc_empty, 0);
-    uint8_t *stage_ptr = smem + off_stage(kF32) + (warp - 4) * stage_bytes(kF32);
-    const uint32_t stage = smem_u32(stage_ptr);
+    uint8_t *stage0_ptr = smem + off_stage(kF32) + (warp - 4) * stage_bytes(kF32);
+    const uint32_t stage0 = smem_u32(stage0_ptr);
+    uint32_t turn = 0;
     int acc = 0;
     bool ok = true;
     for (int seq = 0; ok; ++seq) {
@@ -697,18 +715,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c + 16 * h < U.nq) {
               if (elect_one()) bulk_wait_read<1>();
               __syncwarp();
-              float *row = reinterpret_cast<float *>(stage_ptr + h * 2048) + lane;
+              float *row = reinterpret_cast<float *>(stage0_ptr + turn) + lane;
 #pragma unroll
               for (int j = 0; j < 16; ++j) row[32 * j] = sum[g][16 * h + j];
               fence_async_shared();
               __syncwarp();
               if (pw < P.np && elect_one()) {
                 if (P.accumulate)
-                  tma_add(&M.out, stage + h * 2048, pw, U.q0 + c + 16 * h, U.z);
+                  tma_add(&M.out, stage0 + turn, pw, U.q0 + c + 16 * h, U.z);
                 else
-                  tma_store(&M.out, stage + h * 2048, pw, U.q0 + c + 16 * h, U.z);
+                  tma_store(&M.out, stage0 + turn, pw, U.q0 + c + 16 * h, U.z);
                 bulk_commit();
               }
+              turn ^= kStage;  // the other block next, whichever q's are left out
             }
           }
         }
@@ -722,17 +741,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const int q0 = a ? U.n[0] : 0, nq = a ? U.nq - U.n[0] : min(U.nq, U.n[0]);
+          uint32_t v[32], w[16];
+          if (32 * half < nq) load_columns(t_lane + 256 * buf + 32 * half, v);
           for (int c = 32 * half; c < nq; c += 64) {
-            if (elect_one()) bulk_wait_read<0>();  // the staging block's last copy has left it
+            tc_wait_ld();
+            round_columns<O>(v, U.blocks == 0, w);  // no blocks: nothing was accumulated
+            if (c + 64 < nq)
+              load_columns(t_lane + 256 * buf + c + 64, v);  // on their way during the stores
+            else
+              release(buf);
+            if (elect_one()) bulk_wait_read<0>();  // the block's last copy has left it
             __syncwarp();
-            stage_block<O>(t_lane + 256 * buf + c, U.blocks == 0, stage, lane);
+            stage_rows(w, stage0, lane);
             const int row = U.q0 + q0 + c;
             if (kMode == kGrad || nq - c >= 32) {
               // all 32 q's are stored (the gradient's map ends at its last q)
               fence_async_shared();
               __syncwarp();
               if (pw < P.np && elect_one()) {
-                tma_store(&M.out, stage, pw, row, kMode == kGrad ? U.z : 0);
+                tma_store(&M.out, stage0, pw, row, kMode == kGrad ? U.z : 0);
                 bulk_commit();
               }
             } else {
@@ -743,14 +770,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int q = 8 * i + (lane >> 2);
-                const uint4 x = *reinterpret_cast<const uint4 *>(stage_ptr + stage_offset(q, piece));
+                const uint4 x = *reinterpret_cast<const uint4 *>(stage0_ptr + stage_offset(q, piece));
                 if (q < nq - c && pw + 8 * piece < P.np)
                   *reinterpret_cast<uint4 *>(out + (int64_t)q * P.np) = x;
               }
               __syncwarp();
             }
           }
-          release(buf);
+          if (32 * half >= nq) release(buf);
         }
       }
     }

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluParams P) 
     const T *g_row = gu + (size_t)r * 2 * I, *dh_row = dhp + (size_t)r * I;
     T *o_row = outp + (size_t)r * (kBackward ? 2 * I : I);
     float sum = 0.0f;
-#pragma unroll 2
+#pragma unroll 4
     for (int j = t * V; j < I; j += kRow * V) {
       if constexpr (kVec) {
         Vec8<T> g, u, d, o, o2;
