@@ -45,13 +45,13 @@ constexpr int BP = 256, BQ = 256, BT = 64;  // tile of a CTA pair, depth of a bl
 constexpr int kWide = 2 * BQ;               // q's of a wide unit
 constexpr int kUnitQ = 8;
 constexpr uint32_t kPBytes = 128 * BT * 2;  // a CTA's half of a P tile
-// Bytes of the operand ring, and an epilogue warp's staging: a block of 32 x 32 16-bit
-// values, or two in turn of 16 x 32 binary32 ones.
-constexpr uint32_t ring_bytes(bool f32) { return (f32 ? 160 : 192) * 1024; }
+// Bytes of the operand ring, and of an epilogue warp's staging (gradient): a block of 32 x
+// 32 16-bit values, or two in turn of 16 x 32 binary32 ones.
 constexpr uint32_t kStage = 2048;
-constexpr uint32_t stage_bytes(bool f32) { return f32 ? 2 * kStage : kStage; }
+constexpr uint32_t ring_bytes(int mode, bool f32) { return (mode != kGrad ? 212 : f32 ? 180 : 196) * 1024; }
+constexpr uint32_t stage_bytes(int mode, bool f32) { return mode != kGrad ? 0 : f32 ? 2 * kStage : kStage; }
 constexpr int kSumBlocks = 8;  // blocks of one partial sum (binary32 output): 512 rows
-constexpr int kWideRows = 1024;  // rows from which the gradient takes wide units
+constexpr int kWideRows = 448;  // rows from which the gradient takes wide units
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -113,17 +113,20 @@ struct Shared {
   long long part[33];
   SegTable table;
 };
-constexpr uint32_t off_stage(bool f32) { return ring_bytes(f32); }
-constexpr uint32_t off_shared(bool f32) { return off_stage(f32) + kEpiWarps * stage_bytes(f32); }
-constexpr uint32_t smem_bytes(bool f32) { return off_shared(f32) + sizeof(Shared) + 1024; }
-static_assert(smem_bytes(false) <= 232448 && smem_bytes(true) <= 232448, "shared memory");
+constexpr uint32_t off_shared(int mode, bool f32) {
+  return ring_bytes(mode, f32) + kEpiWarps * stage_bytes(mode, f32);
+}
+constexpr uint32_t smem_bytes(int mode, bool f32) { return off_shared(mode, f32) + sizeof(Shared) + 1024; }
+static_assert(smem_bytes(kFwd, false) <= 232448 && smem_bytes(kGrad, false) <= 232448 &&
+                  smem_bytes(kGrad, true) <= 232448,
+              "shared memory");
 
 // An MN-major operand's column blocks of 64 are a dimension of its map where the columns
 // are a multiple of 64 (`blocked`: one copy brings two blocks), else one copy each.
 struct Maps {
   CUtensorMap p;
   CUtensorMap q[8];  // K-major: boxes of 16, 32, ..., 128 rows; MN-major: of 1, 2 blocks
-  CUtensorMap out;
+  CUtensorMap out;  // gradient
 };
 
 struct GroupedParams {
@@ -310,11 +313,32 @@ __device__ __forceinline__ Unit get_unit(const GroupedParams &P, const SegTable 
 template <class O>
 __device__ __forceinline__ uint32_t pack2(uint32_t lo, uint32_t hi) {
   uint32_t r;
-  if constexpr (sizeof(O) == 2 && !__is_same(O, __half))
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
-  else
+  if constexpr (std::is_same<O, __half>::value)
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
   return r;
+}
+
+// 32 accumulator columns (q) of this warp's 32 lanes (p) -> the rows of a 16-bit output;
+// `out` at the first q and the warp's first p.  Neighbouring lanes swap one of each two
+// q's, so that a lane holds two consecutive p of one row: 4-byte stores, 64 contiguous
+// bytes a row, from registers.  (Staged in shared memory for wider stores or bulk copies,
+// each block cost more in waits and proxy fences than these stores do.)  The extent of p
+// is even and the first p a multiple of 32, so a pair is inside or outside as one.
+template <class O>
+__device__ __forceinline__ void store_columns(const uint32_t *v, uint16_t *out, int64_t pitch,
+                                              int nq, bool inside, int lane) {
+  const int odd = lane & 1;
+  const uint32_t pick = odd ? 0x3276u : 0x5410u;
+  uint16_t *o = out + (lane - odd) + odd * pitch;
+  if (!inside) nq = 0;
+#pragma unroll
+  for (int j = 0; j < 32; j += 2, o += 2 * pitch) {
+    const uint32_t mine = pack2<O>(v[j], v[j + 1]);
+    const uint32_t w = __byte_perm(mine, __shfl_xor_sync(0xffffffffu, mine, 1), pick);
+    if (j + odd < nq) *reinterpret_cast<uint32_t *>(o) = w;
+  }
 }
 
 // 32 accumulator columns (q) of this warp's 32 lanes (p), rounded: w[8h + 2i + (0, 1)] holds
@@ -350,12 +374,12 @@ template <int kMode, class O>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_kernel(const __grid_constant__ Maps M, const GroupedParams P) {
   constexpr bool kF32 = sizeof(O) == 4;
-  constexpr uint32_t kRing = ring_bytes(kF32);
+  constexpr uint32_t kRing = ring_bytes(kMode, kF32);
   constexpr bool kPMn = kMode != kFwd, kQMn = kMode == kGrad;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Shared &S = *reinterpret_cast<Shared *>(smem + off_shared(kF32));
+  Shared &S = *reinterpret_cast<Shared *>(smem + off_shared(kMode, kF32));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t s_ring = smem_u32(smem);
   const uint32_t bar_full = smem_u32(S.full), bar_empty = smem_u32(S.empty);
@@ -385,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     S.abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&M.p);
-    tma_prefetch_desc(&M.out);
+    if (kMode == kGrad) tma_prefetch_desc(&M.out);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(&S.tmem), kTmemCols);
@@ -535,14 +559,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       int acc = 0;
       Ring<kRing> ring;
       bool ok = true;
-      for (int seq = 0; ok; ++seq) {
-        Unit U;
-        if (!take(seq, U)) break;
+      Unit N;  // the next unit, taken while this one's last block is awaited
+      bool next = take(0, N);
+      for (int seq = 0; ok && next; ++seq) {
+        const Unit U = N;
         release_unit(seq);
         if (U.end) break;
+        if (rank != 0 || U.blocks == 0) next = take(seq + 1, N);
         if (rank != 0) continue;  // the odd CTA only follows the unit stream
         const int accs = U.n[1] ? 2 : 1, sums = sums_of(U);
         const uint32_t bytes = block_bytes(U.n[0], U.n[1]);
+        const uint32_t idesc_a = idesc0 | ((uint32_t)(U.n[0] >> 3) << 17);
+        const uint32_t idesc_b = idesc0 | ((uint32_t)(U.n[1] >> 3) << 17);
+        const uint64_t to_b = U.n[0] / 2 * (BT * 2) / 16;  // from one Q tile to the other
         for (int s = 0; s < sums && ok; ++s, acc += accs) {
           for (int a = 0; a < accs && ok; ++a)
             ok = wait(bar_acc_empty + 8 * ((acc + a) & 1), ((uint32_t)((acc + a) >> 1) & 1u) ^ 1u,
@@ -552,16 +581,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int b0 = kF32 ? s * kSumBlocks : 0;
           const int b1 = kF32 ? min(U.blocks, b0 + kSumBlocks) : U.blocks;
           for (int b = b0; b < b1 && ok; ++b) {
+            if (b == U.blocks - 1) next = take(seq + 1, N);
             ok = wait(bar_full + 8 * ring.bar, ring.phase, kWaitLimitNs);
             if (!ok) break;
             tc_fence_after();
             const uint32_t sp = s_ring + ring.place(bytes);
-            uint32_t sq = sp + kPBytes;
+            const uint64_t dp = operand_desc<kPMn>(sp);
+            uint64_t dq = operand_desc<kQMn>(sp + kPBytes);
             const int steps = b == U.blocks - 1 ? (U.rem + 15) >> 4 : BT / 16;
             for (int a = 0; a < accs; ++a) {
-              const uint32_t d = tmem + 256 * ((acc + a) & 1);
-              const uint32_t idesc = idesc0 | ((uint32_t)(U.n[a] >> 3) << 17);
-              const uint64_t dp = operand_desc<kPMn>(sp), dq = operand_desc<kQMn>(sq);
+              const uint32_t d = tmem + 256 * ((acc + a) & 1), idesc = a ? idesc_b : idesc_a;
               mma_pair_f16(d, dp, dq, idesc, b != b0);
               if (steps == BT / 16) {
 #pragma unroll
@@ -571,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 1; j < steps; ++j)
                   mma_pair_f16(d, dp + j * kStep<kPMn>, dq + j * kStep<kQMn>, idesc, 1);
               }
-              sq += U.n[0] / 2 * (BT * 2);
+              dq += to_b;
             }
             tc_commit_pair_mc(bar_empty + 8 * ring.bar, kBoth);
             ring.next_block();
@@ -655,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t t_lane = tmem + ((uint32_t)(32 * quarter) << 16);
     const uint32_t lead_acc_empty = mapa_shared(bar_acc_empty, 0);
-    uint8_t *stage0_ptr = smem + off_stage(kF32) + (warp - 4) * stage_bytes(kF32);
+    uint8_t *stage0_ptr = smem + kRing + (warp - 4) * stage_bytes(kMode, kF32);
     const uint32_t stage0 = smem_u32(stage0_ptr);
     uint32_t turn = 0;
     int acc = 0;
@@ -741,47 +770,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const int q0 = a ? U.n[0] : 0, nq = a ? U.nq - U.n[0] : min(U.nq, U.n[0]);
-          uint32_t v[32], w[16];
-          if (32 * half < nq) load_columns(t_lane + 256 * buf + 32 * half, v);
-          for (int c = 32 * half; c < nq; c += 64) {
-            tc_wait_ld();
-            round_columns<O>(v, U.blocks == 0, w);  // no blocks: nothing was accumulated
-            if (c + 64 < nq)
-              load_columns(t_lane + 256 * buf + c + 64, v);  // on their way during the stores
-            else
-              release(buf);
-            if (elect_one()) bulk_wait_read<0>();  // the block's last copy has left it
-            __syncwarp();
-            stage_rows(w, stage0, lane);
-            const int row = U.q0 + q0 + c;
-            if (kMode == kGrad || nq - c >= 32) {
-              // all 32 q's are stored (the gradient's map ends at its last q)
+          if constexpr (kMode == kGrad) {
+            uint32_t v[32], w[16];
+            if (32 * half < nq) load_columns(t_lane + 256 * buf + 32 * half, v);
+#pragma unroll 1
+            for (int c = 32 * half; c < nq; c += 64) {
+              tc_wait_ld();
+              round_columns<O>(v, U.blocks == 0, w);  // no blocks: nothing was accumulated
+              if (c + 64 < nq)
+                load_columns(t_lane + 256 * buf + c + 64, v);  // on their way during the stores
+              else
+                release(buf);
+              if (elect_one()) bulk_wait_read<0>();  // the block's last copy has left it
+              __syncwarp();
+              stage_rows(w, stage0, lane);
               fence_async_shared();
               __syncwarp();
-              if (pw < P.np && elect_one()) {
-                tma_store(&M.out, stage0, pw, row, kMode == kGrad ? U.z : 0);
+              if (pw < P.np && elect_one()) {  // what passes the extents is left out
+                tma_store(&M.out, stage0, pw, U.q0 + q0 + c, U.z);
                 bulk_commit();
               }
-            } else {
-              // a segment's last rows: what follows belongs to another
-              __syncwarp();
-              const int piece = lane & 3;
-              uint16_t *out = static_cast<uint16_t *>(P.out) + (int64_t)row * P.np + pw + 8 * piece;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int q = 8 * i + (lane >> 2);
-                const uint4 x = *reinterpret_cast<const uint4 *>(stage0_ptr + stage_offset(q, piece));
-                if (q < nq - c && pw + 8 * piece < P.np)
-                  *reinterpret_cast<uint4 *>(out + (int64_t)q * P.np) = x;
-              }
-              __syncwarp();
+            }
+          } else {
+            uint16_t *out = static_cast<uint16_t *>(P.out) + pw + (int64_t)(U.q0 + q0) * P.np;
+#pragma unroll 1
+            for (int c = 32 * half; c < nq; c += 64) {
+              uint32_t v[32];
+              MOE_TMEM_LD_32x32b_X32(t_lane + 256 * buf + c, v);
+              tc_wait_ld();
+              if (c + 64 >= nq) release(buf);
+              store_columns<O>(v, out + (int64_t)c * P.np, P.np, nq - c, pw + lane < P.np, lane);
             }
           }
           if (32 * half >= nq) release(buf);
         }
       }
     }
-    if (elect_one()) bulk_wait();
+    if (kMode == kGrad && elect_one()) bulk_wait();
   }
 
   tc_fence_before();
@@ -812,7 +837,7 @@ EncodeTiledFn encode_fn() {
 
 // Tensor [mats][rows][cols] (cols contiguous) of 2- or 4-byte values, boxes of box_rows x
 // box_cols (of `blocks` column blocks where the columns are split into blocks of 64), the
-// rows of a box swizzled by their length (128, 64 bytes), or not at all.
+// rows of a 16-bit box swizzled by their length (128, 64 bytes).
 bool make_map(CUtensorMap *m, const void *base, uint64_t mats, uint64_t rows, uint64_t cols,
               uint32_t box_rows, uint32_t box_cols, bool f32, uint32_t blocks = 0) {
   EncodeTiledFn fn = encode_fn();
@@ -862,7 +887,7 @@ int launch(const Maps &maps, const GroupedParams &P, int64_t max_units, int num_
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(sms / 2 > 0 ? sms / 2 * 2 : 2));
   cfg.blockDim = dim3(kThreads);
-  constexpr uint32_t kSmem = smem_bytes(sizeof(O) == 4);
+  constexpr uint32_t kSmem = smem_bytes(kMode, sizeof(O) == 4);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = as_stream(stream);
   cudaLaunchAttribute attr[1];
@@ -914,7 +939,6 @@ extern "C" int moe_grouped_gemm(const moe_ggemm_args *a, void *stream) {
   const uint64_t E = a->seg.E, n = a->n, k = a->k, rows = a->seg.rows;
   bool ok = a->trans ? map_mn_major(&maps.p, a->w, E, n, k, 2) : map_k_major(&maps.p, a->w, E, n, k, 128);
   for (int i = 0; i < 8; ++i) ok = ok && map_k_major(&maps.q[i], a->x, 1, rows, P.nt, 16 * (i + 1));
-  ok = ok && make_map(&maps.out, a->out, 1, rows, P.np, 32, 32, false);
   if (!ok) return MOE_ERR_CUDA;
   // row tiles: a full one per 512 rows, and one started in every segment that has rows
   const int64_t started = a->seg.E < a->seg.rows ? a->seg.E : a->seg.rows;
