@@ -59,51 +59,44 @@ __device__ __forceinline__ void store_copy(void *c, int type, int64_t i, float f
   else
     static_cast<float *>(c)[i] = f;
 }
-__device__ __forceinline__ void load_g4(const void *g, int type, int64_t i, float *o) {
-  if (type == MOE_TYPE_F32) {
-    const float4 q = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(g) + i));
-    o[0] = q.x, o[1] = q.y, o[2] = q.z, o[3] = q.w;
-    return;
+// Four values of 16 bits, two to a word, in binary32.
+__device__ __forceinline__ void widen4(uint2 q, bool bf16, float *o) {
+  if (bf16) {
+    o[0] = __uint_as_float(q.x << 16), o[1] = __uint_as_float(q.x & 0xffff0000u);
+    o[2] = __uint_as_float(q.y << 16), o[3] = __uint_as_float(q.y & 0xffff0000u);
+  } else {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&q.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&q.y));
+    o[0] = a.x, o[1] = a.y, o[2] = b.x, o[3] = b.y;
   }
-  const uint2 q = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(g) + i));
-  const uint32_t h[4] = {q.x & 0xffffu, q.x >> 16, q.y & 0xffffu, q.y >> 16};
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    o[j] = type == MOE_TYPE_BF16 ? __uint_as_float(h[j] << 16)
-                                 : __half2float(__ushort_as_half((unsigned short)h[j]));
 }
-__device__ __forceinline__ void store_copy4(void *c, int type, int64_t i, const float *f) {
-  if (type == MOE_TYPE_F32) {
-    *reinterpret_cast<float4 *>(static_cast<float *>(c) + i) = make_float4(f[0], f[1], f[2], f[3]);
-    return;
-  }
-  uint32_t h[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    h[j] = type == MOE_TYPE_BF16 ? f32_to_bf16_bits(f[j])
-                                 : (uint32_t)__half_as_ushort(__float2half_rn(f[j]));
-  *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(c) + i) =
-      make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+__device__ __forceinline__ uint32_t narrow2(float lo, float hi, bool bf16) {
+  uint32_t r;
+  if (bf16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 // Codes: see moe_adamw in include/moe.h.
-// Byte k of w as a float, exactly: as the low bits of 2^23 + byte.
-__device__ __forceinline__ float byte_f32(uint32_t w, int k) {
-  return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 | k)) - 8388608.0f;
+// Byte k of w, less `zero`, as a float, exactly: as the low bits of 2^23 + byte.
+__device__ __forceinline__ float byte_f32(uint32_t w, int k, float zero) {
+  return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 | k)) - (8388608.0f + zero);
 }
 // Code k of a word of four.  m: the sign bits flipped (w ^ 0x80808080) make a byte of c + 128.
 __device__ __forceinline__ float decode_m(uint32_t flipped, int k, float s) {
-  const float q = __fmul_rn(byte_f32(flipped, k) - 128.0f, kInvM);
+  const float q = __fmul_rn(byte_f32(flipped, k, 128.0f), kInvM);
   return __fmul_rn(__fmul_rn(q, fabsf(q)), s);
 }
 __device__ __forceinline__ float decode_r(uint32_t w, int k, float s) {
-  const float q = __fmul_rn(byte_f32(w, k), kInvR);
+  const float q = __fmul_rn(byte_f32(w, k, 0.0f), kInvR);
   return __fmul_rn(__fmul_rn(q, q), s);
 }
 // The whole number c with (c - 1/2)^2 <= z < (c + 1/2)^2, z = levels^2 x / s.  An
 // approximate root, pulled down by more than its error and rounded to the nearest whole
 // number, is c or c - 1; the bound between them, exact in binary32, says which.  Adding
-// 1.5 * 2^23 rounds, and leaves the number in the low bits.
+// 1.5 * 2^23 rounds, and leaves the number in the low byte; the other bits mean nothing.
 __device__ __forceinline__ uint32_t square_code(float x, float inv, float sq) {
   constexpr float kRound = 12582912.0f;
   const float z = __fmul_rn(__fmul_rn(x, inv), sq);
@@ -111,7 +104,11 @@ __device__ __forceinline__ uint32_t square_code(float x, float inv, float sq) {
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(z));  // a subnormal z is code 0 either way
   const float y = __fmaf_rn(root, 1.0f - 0x1p-20f, kRound);
   const float h = __fadd_rn(__fadd_rn(y, -kRound), 0.5f);
-  return (__float_as_uint(y) & 0xffu) + (z >= __fmul_rn(h, h) ? 1u : 0u);
+  return __float_as_uint(y) + (z >= __fmul_rn(h, h) ? 1u : 0u);
+}
+// The low bytes of four words in one.
+__device__ __forceinline__ uint32_t low_bytes(const uint32_t *c) {
+  return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
 }
 __device__ __forceinline__ float block_inverse(float s) {
   return s >= 1.17549435e-38f ? __fdiv_rn(1.0f, s) : 0.0f;
@@ -189,27 +186,83 @@ __device__ __forceinline__ void encode_block(const float *m, const float *r, uin
                                              float &ms, float &rs) {
   ms = block_max(m);
   rs = block_max(r);
-  mc[0] = mc[1] = rc[0] = rc[1] = 0;
+  uint32_t c[8] = {}, d[8] = {};
   if (finite(ms)) {  // else: code 0, which an infinite or NaN scale turns into NaN
     const float inv = block_inverse(ms);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t c = square_code(fabsf(m[j]), inv, kSqM);
-      mc[j >> 2] |= ((m[j] < 0.0f ? 0u - c : c) & 0xffu) << (8 * (j & 3));
+      c[j] = square_code(fabsf(m[j]), inv, kSqM);
+      if (m[j] < 0.0f) c[j] = 0u - c[j];
     }
   }
-  const float inv = finite(rs) ? block_inverse(rs) : 0.0f;
-  const bool ok = finite(rs);
+  if (finite(rs)) {
+    const float inv = block_inverse(rs);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d[j] = square_code(r[j], inv, kSqR) & 0xffu;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (r[j] > 0.0f) d[j] = max(d[j], 1u);
+  mc[0] = low_bytes(c), mc[1] = low_bytes(c + 4);
+  rc[0] = low_bytes(d), rc[1] = low_bytes(d + 4);
+}
+
+// A block of the fast path as it lies in memory, one lane's part.
+template <bool k8Bit>
+struct Raw {
+  float4 p[2], g[2];      // g: 16-bit gradients in .x, .y
+  float4 m[2], v[2];      // 32 bits
+  uint32_t mc[2], rc[2];  // 8 bits
+  float ms, rs;
+};
+template <bool k8Bit>
+__device__ __forceinline__ void load_raw(const Entry &T, int64_t b, int lane, Raw<k8Bit> &R) {
+  const int64_t i0 = b * kBlock;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t i = i0 + place(lane, 4 * h);
+    R.p[h] = __ldcs(reinterpret_cast<const float4 *>(T.p + i));
+    if (T.g_type == MOE_TYPE_F32) {
+      R.g[h] = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(T.g) + i));
+    } else {
+      const float2 q = __ldcs(reinterpret_cast<const float2 *>(static_cast<const uint16_t *>(T.g) + i));
+      R.g[h].x = q.x, R.g[h].y = q.y;
+    }
+    if constexpr (k8Bit) {
+      R.mc[h] = __ldcs(reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(T.m) + i));
+      R.rc[h] = __ldcs(reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(T.v) + i));
+    } else {
+      R.m[h] = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(T.m) + i));
+      R.v[h] = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(T.v) + i));
+    }
+  }
+  if constexpr (k8Bit) {
+    R.ms = T.m_scale[b];
+    R.rs = T.r_scale[b];
+  }
+}
+__device__ __forceinline__ void spread(const float4 *q, float *o) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) o[4 * h] = q[h].x, o[4 * h + 1] = q[h].y, o[4 * h + 2] = q[h].z, o[4 * h + 3] = q[h].w;
+}
+
+// The step of 8 values; r: the new sqrt(v).
+__device__ __forceinline__ void update(const Hyper &H, float gs, const float *g, float *p, float *m,
+                                       float *v, float *r) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    uint32_t d = ok ? square_code(r[j], inv, kSqR) : 0u;
-    if (r[j] > 0.0f) d = max(d, 1u);
-    rc[j >> 2] |= d << (8 * (j & 3));
+    const float x = __fmul_rn(g[j], gs);
+    m[j] = __fadd_rn(__fmul_rn(m[j], H.beta1), __fmul_rn(x, H.alpha1));
+    v[j] = __fadd_rn(__fmul_rn(v[j], H.beta2), __fmul_rn(__fmul_rn(x, x), H.alpha2));
+    r[j] = __fsqrt_rn(v[j]);
+    float inv;  // of the denominator, within an ulp: p is not promised to the bit
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(r[j], H.inv_bc2, H.eps)));
+    p[j] = fmaf(p[j], H.decay, -(m[j] * inv) * H.step);
   }
 }
 
 template <int kMax, bool k8Bit>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     adamw_kernel(const __grid_constant__ Table<kMax> tab, const Hyper H) {
   // the tensor of this CTA's chunk
   int lo = 0, hi = tab.n;
@@ -227,62 +280,95 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t last = min(first + tab.chunk_blocks, blocks);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float gs = H.grad_scale ? *H.grad_scale : 1.0f;
-  for (int64_t b = first + warp; b < last; b += kWarps) {
-    const int64_t i0 = b * kBlock, n = n_all - i0;
-    const bool fast = T.aligned && n >= kBlock;
-    float p[8] = {}, g[8] = {}, m[8] = {}, v[8] = {}, r[8];
-    load_f32(T.p + i0, fast, lane, n, p);
-    if (fast) {
-      load_g4(T.g, T.g_type, i0 + place(lane, 0), g);
-      load_g4(T.g, T.g_type, i0 + place(lane, 4), g + 4);
+  // whole blocks of aligned tensors; with codes, whose arithmetic is long, the next block's
+  // loads are under way while one is worked on
+  const int64_t whole = T.aligned ? min(last, n_all / kBlock) : first;
+  int64_t b = first + warp;
+  Raw<k8Bit> next;
+  if (k8Bit && b < whole) load_raw<k8Bit>(T, b, lane, next);
+  for (; b < whole; b += kWarps) {
+    if (!k8Bit) load_raw<k8Bit>(T, b, lane, next);
+    const Raw<k8Bit> R = next;
+    if (k8Bit && b + kWarps < whole) load_raw<k8Bit>(T, b + kWarps, lane, next);
+    const int64_t i0 = b * kBlock;
+    float p[8], g[8], m[8], v[8], r[8];
+    spread(R.p, p);
+    if (T.g_type == MOE_TYPE_F32) {
+      spread(R.g, g);
     } else {
-      each(lane, n, [&](int j, int i) { g[j] = load_g(T.g, T.g_type, i0 + i); });
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        widen4(make_uint2(__float_as_uint(R.g[h].x), __float_as_uint(R.g[h].y)),
+               T.g_type == MOE_TYPE_BF16, g + 4 * h);
     }
     if constexpr (k8Bit) {
-      uint32_t mc[2], rc[2];
-      load_codes(static_cast<const uint8_t *>(T.m) + i0, fast, lane, n, mc);
-      load_codes(static_cast<const uint8_t *>(T.v) + i0, fast, lane, n, rc);
-      decode_block(mc, rc, T.m_scale[b], T.r_scale[b], m, v);
+      decode_block(R.mc, R.rc, R.ms, R.rs, m, v);
     } else {
-      load_f32(static_cast<const float *>(T.m) + i0, fast, lane, n, m);
-      load_f32(static_cast<const float *>(T.v) + i0, fast, lane, n, v);
+      spread(R.m, m);
+      spread(R.v, v);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float x = H.grad_scale ? __fmul_rn(g[j], gs) : g[j];
-      m[j] = __fadd_rn(__fmul_rn(m[j], H.beta1), __fmul_rn(x, H.alpha1));
-      v[j] = __fadd_rn(__fmul_rn(v[j], H.beta2), __fmul_rn(__fmul_rn(x, x), H.alpha2));
-      r[j] = __fsqrt_rn(v[j]);
-      const float denom = fmaf(r[j], H.inv_bc2, H.eps);
-      p[j] = fmaf(p[j], H.decay, -__fdividef(m[j], denom) * H.step);
-    }
-    store_f32(T.p + i0, fast, lane, n, p);
+    update(H, gs, g, p, m, v, r);
+    store_f32(T.p + i0, true, lane, kBlock, p);
     if (T.copy) {
-      if (fast) {
-        store_copy4(T.copy, T.copy_type, i0 + place(lane, 0), p);
-        store_copy4(T.copy, T.copy_type, i0 + place(lane, 4), p + 4);
+      if (T.copy_type == MOE_TYPE_F32) {
+        store_f32(static_cast<float *>(T.copy) + i0, true, lane, kBlock, p);
       } else {
-        each(lane, n, [&](int j, int i) { store_copy(T.copy, T.copy_type, i0 + i, p[j]); });
+        const bool bf16 = T.copy_type == MOE_TYPE_BF16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          __stcs(reinterpret_cast<uint2 *>(static_cast<uint16_t *>(T.copy) + i0 + place(lane, 4 * h)),
+                 make_uint2(narrow2(p[4 * h], p[4 * h + 1], bf16), narrow2(p[4 * h + 2], p[4 * h + 3], bf16)));
       }
     }
     if constexpr (k8Bit) {
-      if (!fast) {  // places past the tensor's end count for nothing
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (place(lane, j) >= n) m[j] = r[j] = 0.0f;
-      }
       uint32_t mc[2], rc[2];
       float ms, rs;
       encode_block(m, r, mc, rc, ms, rs);
-      store_codes(static_cast<uint8_t *>(T.m) + i0, fast, lane, n, mc);
-      store_codes(static_cast<uint8_t *>(T.v) + i0, fast, lane, n, rc);
+      store_codes(static_cast<uint8_t *>(T.m) + i0, true, lane, kBlock, mc);
+      store_codes(static_cast<uint8_t *>(T.v) + i0, true, lane, kBlock, rc);
       if (lane == 0) {
         T.m_scale[b] = ms;
         T.r_scale[b] = rs;
       }
     } else {
-      store_f32(static_cast<float *>(T.m) + i0, fast, lane, n, m);
-      store_f32(static_cast<float *>(T.v) + i0, fast, lane, n, v);
+      store_f32(static_cast<float *>(T.m) + i0, true, lane, kBlock, m);
+      store_f32(static_cast<float *>(T.v) + i0, true, lane, kBlock, v);
+    }
+  }
+  // the others, value by value
+  for (; b < last; b += kWarps) {
+    const int64_t i0 = b * kBlock, n = n_all - i0;
+    float p[8] = {}, g[8] = {}, m[8] = {}, v[8] = {}, r[8];
+    load_f32(T.p + i0, false, lane, n, p);
+    each(lane, n, [&](int j, int i) { g[j] = load_g(T.g, T.g_type, i0 + i); });
+    if constexpr (k8Bit) {
+      uint32_t mc[2], rc[2];
+      load_codes(static_cast<const uint8_t *>(T.m) + i0, false, lane, n, mc);
+      load_codes(static_cast<const uint8_t *>(T.v) + i0, false, lane, n, rc);
+      decode_block(mc, rc, T.m_scale[b], T.r_scale[b], m, v);
+    } else {
+      load_f32(static_cast<const float *>(T.m) + i0, false, lane, n, m);
+      load_f32(static_cast<const float *>(T.v) + i0, false, lane, n, v);
+    }
+    update(H, gs, g, p, m, v, r);
+    store_f32(T.p + i0, false, lane, n, p);
+    if (T.copy) each(lane, n, [&](int j, int i) { store_copy(T.copy, T.copy_type, i0 + i, p[j]); });
+    if constexpr (k8Bit) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)  // places past the tensor's end count for nothing
+        if (place(lane, j) >= n) m[j] = r[j] = 0.0f;
+      uint32_t mc[2], rc[2];
+      float ms, rs;
+      encode_block(m, r, mc, rc, ms, rs);
+      store_codes(static_cast<uint8_t *>(T.m) + i0, false, lane, n, mc);
+      store_codes(static_cast<uint8_t *>(T.v) + i0, false, lane, n, rc);
+      if (lane == 0) {
+        T.m_scale[b] = ms;
+        T.r_scale[b] = rs;
+      }
+    } else {
+      store_f32(static_cast<float *>(T.m) + i0, false, lane, n, m);
+      store_f32(static_cast<float *>(T.v) + i0, false, lane, n, v);
     }
   }
 }

@@ -110,7 +110,7 @@ struct Shared {
   uint32_t end[kDepth];  // Ring::end of the block that each barrier pair serves
   uint32_t tmem;
   int abort;
-  long long part[33];
+  long long part[64];
   SegTable table;
 };
 constexpr uint32_t off_shared(int mode, bool f32) {

@@ -46,63 +46,61 @@ __device__ __forceinline__ long long warp_scan(long long v, int lane) {
 
 // Fills start and count, and before with the exclusive sums of weight(count).  All
 // threads of the block call it (a multiple of 32, at least 32); `part` is scratch of
-// 33 entries.  Scans run in 64 bits: counts are the caller's and may be anything.
+// 2 x 32 entries.  Scans run in 64 bits: counts are the caller's and may be anything.
+// The weights are first summed for the counts as they are, together with the starts; only
+// if a count is found wrong (negative, above cap, or past the buffer) are they summed again
+// for what is left of it.
 template <class Weight>
 __device__ void build_segments(const SegParams &P, SegTable &T, long long *part, Weight weight,
                                bool report) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int chunks = (P.E + 31) >> 5;
+  long long *part_size = part, *part_weight = part + 32;
+  for (int c = warp; c < chunks; c += warps) {
+    const int e = 32 * c + lane;
+    const int n = e < P.E ? P.counts[e] : 0;
+    const int kept = min(max(n, 0), P.rows);  // weight() takes counts of the buffer
+    const long long size = e < P.E ? ((long long)max(n, 0) + P.align - 1) / P.align * P.align : 0;
+    const long long w = e < P.E ? weight(kept) : 0;
+    const long long s = warp_scan(size, lane), sw = warp_scan(w, lane);
+    if (lane == 31) part_size[c] = s, part_weight[c] = sw;
+    if (e < P.E) {
+      T.count[e] = n;
+      T.start[e] = (int)min(s - size, (long long)INT32_MAX);  // passes the buffer: cut below
+      T.before[e] = (int)(sw - w);
+    }
+  }
+  __syncthreads();
+  const long long size = lane < chunks ? part_size[lane] : 0, w = lane < chunks ? part_weight[lane] : 0;
+  const long long sizes = warp_scan(size, lane), weights = warp_scan(w, lane);
   int bad = 0;
-  for (int pass = 0; pass < 2; ++pass) {  // 0: rows before each segment; 1: weights
-    for (int c = warp; c < chunks; c += warps) {
-      const int e = 32 * c + lane;
-      long long v = 0;
-      if (e < P.E) {
-        if (pass == 0) {
-          int n = P.counts[e];
-          if (n < 0) {
-            bad |= MOE_STATUS_BAD_INDEX;
-            n = 0;
-          }
-          T.count[e] = n;
-          v = ((long long)n + P.align - 1) / P.align * P.align;
-        } else {
-          v = weight(T.count[e]);
-        }
+  for (int c = warp; c < chunks; c += warps) {
+    const int e = 32 * c + lane;
+    const long long base = __shfl_sync(0xffffffffu, sizes - size, c);
+    const int base_w = (int)__shfl_sync(0xffffffffu, weights - w, c);
+    if (e >= P.E) continue;
+    const int n = T.count[e];
+    const long long first = P.cap > 0 ? (long long)e * P.cap : T.start[e] + base;
+    long long kept = max(n, 0);
+    if (P.cap > 0) kept = min(kept, (long long)P.cap);
+    kept = max(0ll, min(kept, P.rows - first));
+    if (n < 0) bad |= MOE_STATUS_BAD_INDEX;
+    if (kept < n) bad |= MOE_STATUS_CAPACITY;
+    T.start[e] = (int)min(first, (long long)P.rows);
+    T.count[e] = (int)kept;
+    T.before[e] += base_w;
+  }
+  const int total = (int)__shfl_sync(0xffffffffu, weights, 31);
+  if (threadIdx.x == 0) T.before[P.E] = total;
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) {
+      long long sum = 0;
+      for (int e = 0; e < P.E; ++e) {
+        T.before[e] = (int)sum;
+        sum += weight(T.count[e]);
       }
-      const long long s = warp_scan(v, lane);
-      if (lane == 31) part[c] = s;
-      if (e < P.E) {
-        if (pass == 0)  // kept as a 31-bit value: what passes the buffer is cut there
-          T.start[e] = (int)min(s - v, (long long)INT32_MAX);
-        else
-          T.before[e] = (int)(s - v);
-      }
+      T.before[P.E] = (int)sum;
     }
-    __syncthreads();
-    if (warp == 0) {
-      const long long v = lane < chunks ? part[lane] : 0;
-      const long long s = warp_scan(v, lane);
-      part[lane] = s - v;
-      if (lane == 31) part[32] = s;
-    }
-    __syncthreads();
-    for (int c = warp; c < chunks; c += warps) {
-      const int e = 32 * c + lane;
-      if (e >= P.E) continue;
-      if (pass == 0) {
-        const long long first = P.cap > 0 ? (long long)e * P.cap : T.start[e] + part[c];
-        const int want = T.count[e];
-        long long n = P.cap > 0 ? min(want, P.cap) : want;
-        n = max(0ll, min(n, P.rows - first));
-        if (n < want) bad |= MOE_STATUS_CAPACITY;
-        T.start[e] = (int)min(first, (long long)P.rows);
-        T.count[e] = (int)n;
-      } else {
-        T.before[e] += (int)part[c];
-      }
-    }
-    if (pass == 1 && threadIdx.x == 0) T.before[P.E] = (int)part[32];
     __syncthreads();
   }
   if (report && bad) status_or(P.status, bad);
