@@ -1,0 +1,97 @@
+"""ExpertTrainer against the same layer by automatic differentiation in 64 bits, and its
+use over several micro-batches and steps."""
+import pytest
+import torch
+
+from combine_moe_route_03_gb300 import api, configs, train
+
+pytestmark = pytest.mark.gpu
+
+SMALL = configs.SMALL_CONTIG.with_(B=77, N=8, K=3, H=512, I=256, n_group=1, topk_group=1, shared=False)
+# Relative 2-norm bounds.  A rounding to bf16 is at most 2^-8 of a value.  The output passes
+# four (gu, whose error the activation at most doubles, h, the rows, their sum), a gradient
+# at most six more (dy is exact, dh, dgu, and those of h and gu in them).
+OUT, GRAD = 5 * 2.0 ** -8, 10 * 2.0 ** -8
+
+
+def make(cfg, seed=0):
+    gen = torch.Generator("cuda").manual_seed(seed)
+    r = lambda *s, scale=1.0: torch.randn(*s, generator=gen, device="cuda") * scale  # noqa: E731
+    W13 = r(cfg.N, 2 * cfg.I, cfg.H, scale=cfg.H ** -0.5).bfloat16().float()
+    W2 = r(cfg.N, cfg.H, cfg.I, scale=cfg.I ** -0.5).bfloat16().float()
+    x, dout = r(cfg.B, cfg.H).bfloat16(), r(cfg.B, cfg.H).bfloat16()
+    route = api.route(cfg, x, r(cfg.N, cfg.H, scale=cfg.H ** -0.5), None)
+    return W13, W2, x, dout, route["topk_idx"], route["topk_w"]
+
+
+def reference(cfg, W13, W2, x, dout, idx, w):
+    W13, W2, x, w = (t.double().requires_grad_() for t in (W13, W2, x, w))
+    out = torch.zeros_like(x)
+    for e in range(cfg.N):
+        t, k = (idx == e).nonzero(as_tuple=True)
+        if len(t):
+            gu = x[t] @ W13[e].t()
+            g, u = gu[:, :cfg.I], gu[:, cfg.I:]
+            out = out.index_add(0, t, w[t, k][:, None] * ((g * torch.sigmoid(g) * u) @ W2[e].t()))
+    out.backward(dout.double())
+    return out.detach(), x.grad, w.grad, W13.grad, W2.grad
+
+
+def off(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+def test_forward_and_gradients_match_autograd(dev):
+    W13, W2, x, dout, idx, w = make(SMALL)
+    t = train.ExpertTrainer(SMALL, W13, W2)
+    out = t.forward(x, idx, w)
+    dx, dw = t.backward(dout)
+    want = reference(SMALL, W13, W2, x, dout, idx, w)
+    assert api.read_status(t.status) == 0
+    assert off(out, want[0]) <= OUT
+    for got, ref in zip((dx, dw, t.grads[0], t.grads[1]), want[1:]):
+        assert off(got, ref) <= GRAD
+
+
+def test_micro_batches_add_up_and_a_step_clears_them(dev):
+    W13, W2, x, dout, idx, w = make(SMALL, 1)
+    a, b = (train.ExpertTrainer(SMALL, W13, W2, state_bits=8, weight_decay=0.0) for _ in range(2))
+    a.forward(x, idx, w)
+    a.backward(dout)
+    one = [g.clone() for g in a.grads]
+    a.forward(x, idx, w)
+    a.backward(dout)
+    for g, h in zip(a.grads, one):
+        assert torch.equal(g, 2 * h)               # doubling is exact
+    b.forward(x, idx, w)
+    b.backward(dout)
+    a.step(grad_scale=torch.tensor(0.5, device=dev))
+    b.step()
+    for p, q, c in zip(a.master, b.master, a.weights):
+        assert torch.equal(p, q) and torch.equal(c, p.bfloat16())
+        assert not torch.equal(p, W13 if p.shape == W13.shape else W2)
+    with pytest.raises(ValueError, match="backward before"):
+        a.step()
+    with pytest.raises(ValueError, match="forward before"):
+        a.backward(dout)
+    a.forward(x, idx, w)
+    a.backward(dout)
+    b.forward(x, idx, w)
+    b.backward(dout)
+    for g, h in zip(a.grads, b.grads):
+        assert torch.equal(g, h)                   # nothing of the last step is left in them
+
+
+@pytest.mark.parametrize("bits", ["8", "32"])
+def test_the_example_learns(dev, bits, capsys):
+    losses = train.main(["--steps", "12", "--state-bits", bits])
+    assert losses[-1] < 0.7 * losses[0]
+
+
+def test_refuses_other_layouts(dev):
+    W13, W2, *_ = make(SMALL)
+    for cfg in (SMALL.with_(layout=configs.MASKED, cap=128), SMALL.with_(n_phys=10)):
+        with pytest.raises(ValueError, match="expected"):
+            train.ExpertTrainer(cfg, W13, W2)
+    with pytest.raises(ValueError, match="expected"):
+        train.ExpertTrainer(SMALL, W2, W13)
