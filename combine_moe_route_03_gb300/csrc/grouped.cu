@@ -103,7 +103,7 @@ struct Ring {
 };
 
 struct Shared {
-  uint64_t full[kDepth], empty[kDepth], tail[kDepth], peer[kDepth];
+  uint64_t full[kDepth], empty[kDepth], tail[kDepth];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t unit_full[kUnitQ], unit_empty[kUnitQ];
   Unit unit[kUnitQ];
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t s_ring = smem_u32(smem);
   const uint32_t bar_full = smem_u32(S.full), bar_empty = smem_u32(S.empty);
-  const uint32_t bar_tail = smem_u32(S.tail), bar_peer = smem_u32(S.peer);
+  const uint32_t bar_tail = smem_u32(S.tail);
   const uint32_t bar_acc_full = smem_u32(S.acc_full), bar_acc_empty = smem_u32(S.acc_empty);
   const uint32_t bar_unit_full = smem_u32(S.unit_full), bar_unit_empty = smem_u32(S.unit_empty);
   volatile int *abort = &S.abort;
@@ -392,10 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kDepth; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_full + 8 * s, kMode == kGrad ? 2 : 1);  // gradient: each CTA arrives
       mbar_init(bar_empty + 8 * s, 1);
       mbar_init(bar_tail + 8 * s, 1);
-      mbar_init(bar_peer + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar_acc_full + 8 * b, 1);
@@ -535,7 +534,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(bar_tail + 8 * ring.bar, bytes);
             load(std::false_type{}, bar_tail + 8 * ring.bar);
           } else {
-            if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * ring.bar, 2 * bytes);
+            if (rank == 0)
+              mbar_arrive_expect_tx(bar_full + 8 * ring.bar, 2 * bytes);
+            else if (kMode == kGrad)
+              mbar_arrive_remote(lead_full + 8 * ring.bar);
             load(std::true_type{}, lead_full + 8 * ring.bar);
           }
           ++blocks;
@@ -633,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (kMode == kGrad && warp == 3) {
       // -------------------------------------- rows past the segment's last
-      const uint32_t lead_peer = mapa_shared(bar_peer, 0);
+      const uint32_t lead_full = mapa_shared(bar_full, 0);
       Ring<kRing> ring;
       uint32_t parity = 0;  // of each tail and peer barrier
       for (int seq = 0;; ++seq) {
@@ -662,18 +664,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_async_shared();
         __syncwarp();
-        // the odd CTA's zeros are known to the even one's warp, which then opens the block
-        if (rank == 1) {
-          if (lane == 0) mbar_arrive_cluster(lead_peer + 8 * bar);
-        } else {
-          const bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar_peer + 8 * bar, (parity >> bar) & 1u,
-                                                                    abort, unit_limit));
-          if (!ok) {
-            fail();
-            break;
-          }
-          if (lane == 0) mbar_arrive(bar_full + 8 * bar);
-        }
+        // The fence has the zeros in this SM's shared memory, where the pair's MMAs read them.
+        // (An arrival with cluster-wide release would also wait for whatever the SM is storing:
+        // 2000 to 3700 cycles a unit.)
+        if (lane == 0) mbar_arrive_remote(lead_full + 8 * bar);
         parity ^= 1u << bar;
       }
     }
