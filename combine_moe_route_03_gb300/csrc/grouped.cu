@@ -51,7 +51,7 @@ constexpr uint32_t kStage = 2048;
 constexpr uint32_t ring_bytes(int mode, bool f32) { return (mode != kGrad ? 212 : f32 ? 180 : 196) * 1024; }
 constexpr uint32_t stage_bytes(int mode, bool f32) { return mode != kGrad ? 0 : f32 ? 2 * kStage : kStage; }
 constexpr int kSumBlocks = 8;  // blocks of one partial sum (binary32 output): 512 rows
-constexpr int kWideRows = 448;  // rows from which the gradient takes wide units
+constexpr int kWideRows = 896;  // rows from which the gradient takes wide units
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -110,7 +110,7 @@ struct Shared {
   uint32_t end[kDepth];  // Ring::end of the block that each barrier pair serves
   uint32_t tmem;
   int abort;
-  long long part[64];
+  int part[64];
   SegTable table;
 };
 constexpr uint32_t off_shared(int mode, bool f32) {
@@ -201,6 +201,11 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
+// The cluster's threads meet; nothing of their memory is ordered by it (a release would
+// first wait for every store).
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 // One lane of a converged warp, chosen so that the compiler knows it is one: the
 // descriptors of MMAs and copies sit in uniform registers, and behind `lane == 0` each
 // would be issued through a loop over the lanes (80 cycles an MMA instead of 45).
@@ -252,11 +257,12 @@ constexpr uint64_t kStep = kMnMajor ? 2048 / 16 : 32 / 16;
 // Rows of a segment's row tiles: one tile of up to 256 (one accumulator, the other one
 // takes the next unit's MMAs meanwhile), else the fewest of up to 512 (both), evened out.
 __device__ __forceinline__ int tile_rows(int count) {
+  if (count <= kWide) return (count + 31) / 32 * 32;
   const int tiles = (count + kWide - 1) / kWide;
   return ((count + tiles - 1) / tiles + 31) / 32 * 32;
 }
 __device__ __forceinline__ int row_tiles(int count) {
-  if (count <= 0) return 0;
+  if (count <= kWide) return count > 0;
   const int rows = tile_rows(count);
   return (count + rows - 1) / rows;
 }
@@ -284,11 +290,12 @@ template <int kMode, bool kF32>
 __device__ __forceinline__ Unit get_unit(const GroupedParams &P, const SegTable &T, int u,
                                          int p_tiles, int &e) {
   Unit U = {};
-  if (e < 0 || u >= T.before[e + 1] * p_tiles) e = find_segment(T, P.seg.E, u / p_tiles);
+  if (e < 0 || u >= T.before[e + 1] * p_tiles) e = find_segment(T, P.seg.E, u, p_tiles);
   const int tiles = T.before[e + 1] - T.before[e];  // q tiles of the segment
-  const int local = u - T.before[e] * p_tiles, qt = local % tiles, count = T.count[e];
+  const int local = u - T.before[e] * p_tiles, count = T.count[e];
+  const int pt = tiles == 1 ? local : local / tiles, qt = local - pt * tiles;
   U.z = e;
-  U.p0 = local / tiles * BP;
+  U.p0 = pt * BP;
   if constexpr (kMode == kGrad) {
     const int q = grad_q<kF32>(P.nq, count);
     U.q0 = qt * q;
@@ -390,25 +397,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint16_t kBoth = 3;
   const int rank = (int)cluster_ctarank();
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kDepth; ++s) {
-      mbar_init(bar_full + 8 * s, kMode == kGrad ? 2 : 1);  // gradient: each CTA arrives
-      mbar_init(bar_empty + 8 * s, 1);
-      mbar_init(bar_tail + 8 * s, 1);
+  if (warp == 0) {  // a lane a barrier
+    if (lane < kDepth) {
+      mbar_init(bar_full + 8 * lane, kMode == kGrad ? 2 : 1);  // gradient: each CTA arrives
+      mbar_init(bar_empty + 8 * lane, 1);
+      mbar_init(bar_tail + 8 * lane, 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(bar_acc_full + 8 * b, 1);
-      mbar_init(bar_acc_empty + 8 * b, 2 * kEpiWarps);  // both CTAs' epilogue warps
+    if (lane < 2) {
+      mbar_init(bar_acc_full + 8 * lane, 1);
+      mbar_init(bar_acc_empty + 8 * lane, 2 * kEpiWarps);  // both CTAs' epilogue warps
     }
-    for (int q = 0; q < kUnitQ; ++q) {
-      mbar_init(bar_unit_full + 8 * q, 1);
+    if (lane < kUnitQ) {
+      mbar_init(bar_unit_full + 8 * lane, 1);
       // producer, MMA, epilogue warps, and the gradient's tail warp
-      mbar_init(bar_unit_empty + 8 * q, 2 + kEpiWarps + (kMode == kGrad ? 1 : 0));
+      mbar_init(bar_unit_empty + 8 * lane, 2 + kEpiWarps + (kMode == kGrad ? 1 : 0));
     }
-    S.abort = 0;
+    if (lane == 0) {
+      S.abort = 0;
+      tma_prefetch_desc(&M.p);
+      if (kMode == kGrad) tma_prefetch_desc(&M.out);
+    }
     fence_mbar_init();
-    tma_prefetch_desc(&M.p);
-    if (kMode == kGrad) tma_prefetch_desc(&M.out);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(&S.tmem), kTmemCols);
@@ -426,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cluster_id_x() == 0 && rank == 0);
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // both CTAs' barriers exist before anything targets them
+  cluster_meet();  // both CTAs' barriers exist before anything targets them
   tc_fence_after();
   const uint32_t tmem = S.tmem;
   const int p_tiles = (P.np + BP - 1) / BP;
@@ -805,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // the even CTA's MMAs read the odd CTA's shared memory to the end
+  cluster_meet();  // the even CTA's MMAs read the odd CTA's shared memory to the end
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, kTmemCols);
 }

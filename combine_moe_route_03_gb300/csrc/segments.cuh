@@ -34,53 +34,42 @@ struct SegTable {
   int before[kMaxSegments + 1]; // rows (or units) of the segments before this one
 };
 
-// Inclusive scan over a warp.
-__device__ __forceinline__ long long warp_scan(long long v, int lane) {
+// Inclusive sums over a warp, held at INT32_MAX: counts are the caller's and may be
+// anything, and a sum that large lies past every buffer.
+__device__ __forceinline__ int warp_scan(int v, int lane) {
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += o;
+    const int o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v = (int)min((unsigned)v + (unsigned)o, (unsigned)INT32_MAX);
   }
   return v;
 }
 
+// The sum before this lane's, of an inclusive scan (held sums cannot be subtracted).
+__device__ __forceinline__ int before_lane(int s, int lane) {
+  const int o = __shfl_up_sync(0xffffffffu, s, 1);
+  return lane ? o : 0;
+}
+
 // Fills start and count, and before with the exclusive sums of weight(count).  All
 // threads of the block call it (a multiple of 32, at least 32); `part` is scratch of
-// 2 x 32 entries.  Scans run in 64 bits: counts are the caller's and may be anything.
-// The weights are first summed for the counts as they are, together with the starts; only
-// if a count is found wrong (negative, above cap, or past the buffer) are they summed again
-// for what is left of it.
+// 2 x 32 entries.  The weights are first summed for the counts as they are, together with
+// the starts; only if a count is found wrong (negative, above cap, or past the buffer) are
+// they summed again for what is left of it.
 template <class Weight>
-__device__ void build_segments(const SegParams &P, SegTable &T, long long *part, Weight weight,
+__device__ void build_segments(const SegParams &P, SegTable &T, int *part, Weight weight,
                                bool report) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int chunks = (P.E + 31) >> 5;
-  long long *part_size = part, *part_weight = part + 32;
-  for (int c = warp; c < chunks; c += warps) {
-    const int e = 32 * c + lane;
-    const int n = e < P.E ? P.counts[e] : 0;
-    const int kept = min(max(n, 0), P.rows);  // weight() takes counts of the buffer
-    const long long size = e < P.E ? ((long long)max(n, 0) + P.align - 1) / P.align * P.align : 0;
-    const long long w = e < P.E ? weight(kept) : 0;
-    const long long s = warp_scan(size, lane), sw = warp_scan(w, lane);
-    if (lane == 31) part_size[c] = s, part_weight[c] = sw;
-    if (e < P.E) {
-      T.count[e] = n;
-      T.start[e] = (int)min(s - size, (long long)INT32_MAX);  // passes the buffer: cut below
-      T.before[e] = (int)(sw - w);
-    }
-  }
-  __syncthreads();
-  const long long size = lane < chunks ? part_size[lane] : 0, w = lane < chunks ? part_weight[lane] : 0;
-  const long long sizes = warp_scan(size, lane), weights = warp_scan(w, lane);
+  auto size_of = [&](int n) {  // rows of the segment with its padding
+    if (P.align == 1) return n;
+    const long long s = ((long long)n + P.align - 1) / P.align * P.align;
+    return (int)min(s, (long long)INT32_MAX);
+  };
   int bad = 0;
-  for (int c = warp; c < chunks; c += warps) {
-    const int e = 32 * c + lane;
-    const long long base = __shfl_sync(0xffffffffu, sizes - size, c);
-    const int base_w = (int)__shfl_sync(0xffffffffu, weights - w, c);
-    if (e >= P.E) continue;
-    const int n = T.count[e];
-    const long long first = P.cap > 0 ? (long long)e * P.cap : T.start[e] + base;
+  // One entry: its first row is known; counts what is kept of it.
+  auto settle = [&](int e, int n, int start) {
+    const long long first = P.cap > 0 ? (long long)e * P.cap : start;
     long long kept = max(n, 0);
     if (P.cap > 0) kept = min(kept, (long long)P.cap);
     kept = max(0ll, min(kept, P.rows - first));
@@ -88,30 +77,63 @@ __device__ void build_segments(const SegParams &P, SegTable &T, long long *part,
     if (kept < n) bad |= MOE_STATUS_CAPACITY;
     T.start[e] = (int)min(first, (long long)P.rows);
     T.count[e] = (int)kept;
-    T.before[e] += base_w;
+  };
+  for (int c = warp; c < chunks; c += warps) {
+    const int e = 32 * c + lane;
+    const int n = e < P.E ? P.counts[e] : 0;
+    const int size = size_of(max(n, 0));
+    const int w = e < P.E ? weight(min(max(n, 0), P.rows)) : 0;
+    const int s = warp_scan(size, lane), sw = warp_scan(w, lane), start = before_lane(s, lane);
+    if (e < P.E) {
+      T.before[e] = sw - w;
+      if (chunks == 1) {
+        settle(e, n, start);
+      } else {
+        T.count[e] = n;
+        T.start[e] = start;
+      }
+    }
+    if (lane == 31) {
+      part[c] = s, part[32 + c] = sw;
+      if (chunks == 1) T.before[P.E] = sw;
+    }
   }
-  const int total = (int)__shfl_sync(0xffffffffu, weights, 31);
-  if (threadIdx.x == 0) T.before[P.E] = total;
+  if (chunks > 1) {
+    __syncthreads();
+    const int size = lane < chunks ? part[lane] : 0, w = lane < chunks ? part[32 + lane] : 0;
+    const int sizes = before_lane(warp_scan(size, lane), lane), weights = warp_scan(w, lane);
+    const int total = __shfl_sync(0xffffffffu, weights, 31);
+    for (int c = warp; c < chunks; c += warps) {
+      const int e = 32 * c + lane;
+      const int base = __shfl_sync(0xffffffffu, sizes, c);
+      const int base_w = __shfl_sync(0xffffffffu, weights - w, c);
+      if (e >= P.E) continue;
+      settle(e, T.count[e], (int)min((unsigned)T.start[e] + (unsigned)base, (unsigned)INT32_MAX));
+      T.before[e] += base_w;
+    }
+    if (threadIdx.x == 0) T.before[P.E] = total;
+  }
   if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0) {
-      long long sum = 0;
+      int sum = 0;
       for (int e = 0; e < P.E; ++e) {
-        T.before[e] = (int)sum;
+        T.before[e] = sum;
         sum += weight(T.count[e]);
       }
-      T.before[P.E] = (int)sum;
+      T.before[P.E] = sum;
     }
     __syncthreads();
   }
   if (report && bad) status_or(P.status, bad);
 }
 
-// The segment that holds item i of the `before` sums: the last e with before[e] <= i.
-__device__ __forceinline__ int find_segment(const SegTable &T, int E, int i) {
-  int lo = 0, hi = E;  // before[lo] <= i < before[hi]
+// The segment that holds item i where each of the `before` sums counts `scale` items: the
+// last e with before[e] * scale <= i.
+__device__ __forceinline__ int find_segment(const SegTable &T, int E, int i, int scale = 1) {
+  int lo = 0, hi = E;  // before[lo] * scale <= i < before[hi] * scale
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (T.before[mid] <= i)
+    if (T.before[mid] * scale <= i)
       lo = mid;
     else
       hi = mid;

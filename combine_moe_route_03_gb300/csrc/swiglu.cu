@@ -72,7 +72,7 @@ __device__ __forceinline__ float backward_one(float g, float u, float dh, float 
 template <class T, bool kBackward, bool kVec, int kRow>
 __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluParams P) {
   __shared__ SegTable table;
-  __shared__ long long part[64];
+  __shared__ int part[64];
   __shared__ float warp_sum[kThreads / 32];
   int total = P.seg.rows;
   if (P.seg.counts) {
