@@ -212,20 +212,19 @@ def ptr(t, host: bool = False) -> int | None:
     return int(t)
 
 
-def ptrs(*tensors) -> list:
-    """ptr of each device tensor (None stays None), the current device looked up once."""
-    out, dev = [], -1
+def ptrs(*tensors) -> tuple[list, int]:
+    """ptr of each device tensor (None stays None), and the handle of the current device's
+    current stream: the device and its stream are looked up once."""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    out = []
     for t in tensors:
         if t is None:
             out.append(None)
-            continue
-        if dev < 0 and t.is_cuda:
-            dev = torch.cuda.current_device()
-        if t.is_cuda and t.get_device() == dev and t.is_contiguous():
+        elif t.get_device() == dev and t.is_contiguous():
             out.append(t.data_ptr())
         else:
             out.append(ptr(t))  # raises
-    return out
+    return out, torch._C._cuda_getCurrentRawStream(dev)
 
 
 def stream_ptr(stream=None) -> int:

@@ -382,12 +382,15 @@ def _is(t, what: str, dtype: torch.dtype, shape: tuple) -> None:
         _expect(t, what, (dtype,), shape)
 
 
-def _on(stream, *tensors) -> int:
-    """_ordered for calls that may take another stream: its inputs and outputs too are
-    kept from reuse until that stream is done with them."""
-    if stream is None:      # the current device's current stream
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    return _ordered(stream, *tensors)
+def _is_counts(counts) -> None:
+    if not (isinstance(counts, torch.Tensor) and counts.dtype == torch.int32 and counts.dim() == 1):
+        _expect(counts, "counts", (torch.int32,), (None,))
+
+
+def _on(stream, current: int, *tensors) -> int:
+    """_ordered for calls that may take another stream than the current one (`current`):
+    its inputs and outputs too are kept from reuse until that stream is done with them."""
+    return current if stream is None else _ordered(stream, *tensors)
 
 
 def _segments(counts: torch.Tensor | None, address: int | None, align: int, cap: int,
@@ -405,7 +408,8 @@ def grouped_gemm(x: torch.Tensor, w: torch.Tensor, counts: torch.Tensor, trans: 
     (align 128: a contiguous dispatch, 1: packed rows; cap: a masked dispatch).  Rows
     outside the segments are not written.  status: int32 word for what the device finds
     wrong with the counts (new_status; without one it is not reported)."""
-    _expect(w, "w", _HALF, (None, None, None))
+    if w.dim() != 3 or w.dtype not in _HALF:
+        _expect(w, "w", _HALF, (None, None, None))
     E, n, k = w.shape
     red, cols = (n, k) if trans else (k, n)
     rows = x.shape[0]
@@ -415,10 +419,10 @@ def grouped_gemm(x: torch.Tensor, w: torch.Tensor, counts: torch.Tensor, trans: 
         out = torch.empty((rows, cols), dtype=w.dtype, device=x.device)
     else:
         _is(out, "out", w.dtype, (rows, cols))
-    pc, px, pw, po, ps = ptrs(counts, x, w, out, status)
+    (pc, px, pw, po, ps), s = ptrs(counts, x, w, out, status)
     a = GgemmArgs(_segments(counts, pc, align, cap, rows), n, k, int(trans), _TYPES[w.dtype], px,
                   pw, po, ps, num_sms_)
-    check(load().moe_grouped_gemm(ctypes.byref(a), _on(stream, x, w, counts, out, status)),
+    check(load().moe_grouped_gemm(ctypes.byref(a), _on(stream, s, x, w, counts, out, status)),
           "moe_grouped_gemm")
     return out
 
@@ -435,7 +439,7 @@ def grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, counts: torch.Tensor, align
     rows, n = dy.shape
     _expect(x, "x", (dy.dtype,), (rows, None))
     k = x.shape[1]
-    _expect(counts, "counts", (torch.int32,), (None,))
+    _is_counts(counts)
     E = counts.shape[0]
     if out is None:
         if accumulate:
@@ -444,10 +448,10 @@ def grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, counts: torch.Tensor, align
     _expect(out, "out", (dy.dtype, torch.float32) if out_dtype is None else (out_dtype,), (E, n, k))
     if accumulate and out.dtype != torch.float32:
         raise ValueError("accumulate: out of dtype torch.float32 expected")
-    pc, pd, px, po, ps = ptrs(counts, dy, x, out, status)
+    (pc, pd, px, po, ps), s = ptrs(counts, dy, x, out, status)
     a = WgradArgs(_segments(counts, pc, align, cap, rows), n, k, _TYPES[dy.dtype],
                   _TYPES[out.dtype], int(accumulate), pd, px, po, ps, num_sms_)
-    check(load().moe_grouped_wgrad(ctypes.byref(a), _on(stream, dy, x, counts, out, status)),
+    check(load().moe_grouped_wgrad(ctypes.byref(a), _on(stream, s, dy, x, counts, out, status)),
           "moe_grouped_wgrad")
     return out
 
@@ -459,22 +463,23 @@ def swiglu(gu: torch.Tensor, row_w: torch.Tensor | None = None,
     """moe_swiglu: gu bf16 / fp16 [rows][2I] (gate, then up columns) -> w silu(g) u
     [rows][I]; row_w fp32 [rows] (default 1).  counts / align / cap / status: only the
     rows of these segments (see grouped_gemm); default all rows."""
-    _expect(gu, "gu", _HALF, (None, None))
+    if gu.dim() != 2 or gu.dtype not in _HALF:
+        _expect(gu, "gu", _HALF, (None, None))
     rows, I2 = gu.shape
     if I2 % 2:
         raise ValueError("gu: an even number of columns expected")
     if row_w is not None:
         _is(row_w, "row_w", torch.float32, (rows,))
     if counts is not None:
-        _expect(counts, "counts", (torch.int32,), (None,))
+        _is_counts(counts)
     if out is None:
         out = torch.empty((rows, I2 // 2), dtype=gu.dtype, device=gu.device)
     else:
         _is(out, "out", gu.dtype, (rows, I2 // 2))
-    pc, pg, pw, po, ps = ptrs(counts, gu, row_w, out, status)
+    (pc, pg, pw, po, ps), s = ptrs(counts, gu, row_w, out, status)
     a = SwigluArgs(_segments(counts, pc, align, cap, rows), I2 // 2, _TYPES[gu.dtype], pg, None,
                    pw, po, None, ps)
-    check(load().moe_swiglu(ctypes.byref(a), _on(stream, gu, row_w, counts, out, status)),
+    check(load().moe_swiglu(ctypes.byref(a), _on(stream, s, gu, row_w, counts, out, status)),
           "moe_swiglu")
     return out
 
@@ -485,7 +490,8 @@ def swiglu_backward(gu: torch.Tensor, dh: torch.Tensor, row_w: torch.Tensor | No
                     status: torch.Tensor | None = None, stream=None):
     """moe_swiglu_backward: dh [rows][I], the gradient of swiglu's output -> (dgu
     [rows][2I], drow_w fp32 [rows], or None without row_w).  dgu may be gu itself."""
-    _expect(gu, "gu", _HALF, (None, None))
+    if gu.dim() != 2 or gu.dtype not in _HALF:
+        _expect(gu, "gu", _HALF, (None, None))
     rows, I2 = gu.shape
     if I2 % 2:
         raise ValueError("gu: an even number of columns expected")
@@ -497,16 +503,16 @@ def swiglu_backward(gu: torch.Tensor, dh: torch.Tensor, row_w: torch.Tensor | No
     if drow_w is not None:
         _is(drow_w, "drow_w", torch.float32, (rows,))
     if counts is not None:
-        _expect(counts, "counts", (torch.int32,), (None,))
+        _is_counts(counts)
     if dgu is None:
         dgu = torch.empty_like(gu)
     else:
         _is(dgu, "dgu", gu.dtype, (rows, I2))
-    pc, pg, pd, pw, po, pr, ps = ptrs(counts, gu, dh, row_w, dgu, drow_w, status)
+    (pc, pg, pd, pw, po, pr, ps), s = ptrs(counts, gu, dh, row_w, dgu, drow_w, status)
     a = SwigluArgs(_segments(counts, pc, align, cap, rows), I2 // 2, _TYPES[gu.dtype], pg, pd, pw,
                    po, pr, ps)
     check(load().moe_swiglu_backward(ctypes.byref(a),
-                                     _on(stream, gu, dh, row_w, counts, dgu, drow_w, status)),
+                                     _on(stream, s, gu, dh, row_w, counts, dgu, drow_w, status)),
           "moe_swiglu_backward")
     return dgu, drow_w
 
@@ -568,7 +574,8 @@ class AdamW:
         parameter; grad_scale: fp32 device scalar that multiplies every gradient."""
         if len(grads) != len(self.params):
             raise ValueError(f"{len(self.params)} gradients expected, got {len(grads)}")
-        for t, p, g, a in zip(self._table, self.params, grads, ptrs(*grads)):
+        addresses, s = ptrs(*grads)
+        for t, p, g, a in zip(self._table, self.params, grads, addresses):
             kind = _TYPES.get(g.dtype)
             if kind is None or g.shape != p.shape:
                 raise ValueError(f"gradient: {tuple(p.shape)} of dtype bf16, fp16 or fp32 "
@@ -581,7 +588,7 @@ class AdamW:
         cfg = AdamwCfg(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
                        self.steps + 1, self.state_bits, ptr(grad_scale))
         check(load().moe_adamw(ctypes.byref(cfg), self._table, len(self.params),
-                               _on(stream, *grads, grad_scale)), "moe_adamw")
+                               _on(stream, s, *grads, grad_scale)), "moe_adamw")
         self.steps += 1
 
     def state(self, stream=None):
@@ -591,9 +598,10 @@ class AdamW:
             return self.m, self.v
         m, v = (torch.empty(self.numel, dtype=torch.float32, device=self.m_code.device)
                 for _ in range(2))
-        check(load().moe_adamw_decode(self.numel, ptr(self.m_code), ptr(self.m_scale),
-                                      ptr(self.r_code), ptr(self.r_scale), ptr(m), ptr(v),
-                                      _on(stream, m, v)), "moe_adamw_decode")
+        (mc, ms, rc, rs, pm, pv), s = ptrs(self.m_code, self.m_scale, self.r_code, self.r_scale,
+                                           m, v)
+        check(load().moe_adamw_decode(self.numel, mc, ms, rc, rs, pm, pv, _on(stream, s, m, v)),
+              "moe_adamw_decode")
         return m, v
 
     def load_state(self, m: torch.Tensor, v: torch.Tensor, steps: int, stream=None) -> None:
