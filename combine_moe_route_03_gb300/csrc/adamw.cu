@@ -6,8 +6,9 @@
 // every load of the warp is contiguous); the block's largest magnitude is one warp
 // reduction, and old codes are read and new ones written in the same pass.  The tensors'
 // table travels as a kernel parameter: nothing is kept on the device between calls.
-// Bound by memory: 28 bytes a value with binary32 moments, 16-bit gradients and a 16-bit
-// copy, 16 with 8-bit moments.
+// Bound by memory with binary32 moments: 28 bytes a value with 16-bit gradients and a 16-bit
+// copy, 7.0 TB/s over 201 M values (803 us).  With 8-bit moments 16 bytes a value and 97
+// instructions: 6.1 TB/s (526 us), about 80 % of the issue slots.
 #include <cuda_fp16.h>
 #include <math.h>
 #include <string.h>
@@ -18,8 +19,13 @@ namespace moe {
 namespace {
 
 constexpr int kBlock = 256;          // values of one 8-bit block
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+// Threads of a CTA: the step on codes is long arithmetic on loads made a block ahead, and
+// runs best in small CTAs, each replaced as it ends (201 M values: 526 us in CTAs of 32, 582
+// of 128, 654 of 256); the step on binary32 moments is memory alone (803 us in CTAs of 256;
+// 854 against 827 in CTAs of 64 and 64 blocks a CTA).
+constexpr int threads_of(bool bits8) { return bits8 ? 32 : 256; }
+constexpr int kChunk = 16;  // blocks of a CTA, at most (64: 826 us and 551 us)
+constexpr int kCodesThreads = 256;
 constexpr float kInvM = (float)(1.0 / 127), kInvR = (float)(1.0 / 255);
 constexpr float kSqM = 127.0f * 127.0f, kSqR = 255.0f * 255.0f;
 
@@ -115,10 +121,10 @@ __device__ __forceinline__ float block_inverse(float s) {
 }
 // Largest magnitude of the warp's block; a NaN wins over every number.
 __device__ __forceinline__ float block_max(const float *x) {
-  uint32_t b = 0;
+  float b = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) b = max(b, __float_as_uint(x[j]) & 0x7fffffffu);
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, b));
+  for (int j = 0; j < 8; ++j) asm("max.NaN.f32 %0, %1, %2;" : "=f"(b) : "f"(b), "f"(fabsf(x[j])));
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(b)));
 }
 __device__ __forceinline__ bool finite(float s) { return s <= 3.402823466e+38f; }
 
@@ -247,11 +253,15 @@ __device__ __forceinline__ void spread(const float4 *q, float *o) {
 }
 
 // The step of 8 values; r: the new sqrt(v).
-__device__ __forceinline__ void update(const Hyper &H, float gs, const float *g, float *p, float *m,
+__device__ __forceinline__ void update(const Hyper &H, float gs, float *g, float *p, float *m,
                                        float *v, float *r) {
+  if (H.grad_scale) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] = __fmul_rn(g[j], gs);
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float x = __fmul_rn(g[j], gs);
+    const float x = g[j];
     m[j] = __fadd_rn(__fmul_rn(m[j], H.beta1), __fmul_rn(x, H.alpha1));
     v[j] = __fadd_rn(__fmul_rn(v[j], H.beta2), __fmul_rn(__fmul_rn(x, x), H.alpha2));
     r[j] = __fsqrt_rn(v[j]);
@@ -262,8 +272,9 @@ __device__ __forceinline__ void update(const Hyper &H, float gs, const float *g,
 }
 
 template <int kMax, bool k8Bit>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(threads_of(k8Bit), 768 / threads_of(k8Bit))
     adamw_kernel(const __grid_constant__ Table<kMax> tab, const Hyper H) {
+  constexpr int kWarps = threads_of(k8Bit) / 32;
   // the tensor of this CTA's chunk
   int lo = 0, hi = tab.n;
   while (hi - lo > 1) {
@@ -374,9 +385,10 @@ __global__ void __launch_bounds__(kThreads, 3)
 }
 
 template <bool kEncode>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kCodesThreads)
     codes_kernel(int64_t n_all, uint8_t *m_code, float *m_scale, uint8_t *r_code, float *r_scale,
                  float *mp, float *vp) {
+  constexpr int kWarps = kCodesThreads / 32;
   const int64_t blocks = (n_all + kBlock - 1) / kBlock;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int64_t b = (int64_t)blockIdx.x * kWarps + warp; b < blocks; b += (int64_t)gridDim.x * kWarps) {
@@ -418,10 +430,10 @@ int launch(const moe_adamw_tensor *t, int n, bool bits8, const Hyper &H, cudaStr
   tab.n = n;
   int64_t blocks = 0;
   for (int i = 0; i < n; ++i) blocks += (t[i].n + kBlock - 1) / kBlock;
-  // 64 blocks a CTA where there is work for several rounds of CTAs, fewer (one block a
-  // warp) where the step is small
-  int chunk = 64;
-  while (chunk > kWarps && blocks / chunk < 8 * device_sm_count()) chunk >>= 1;
+  // fewer blocks a CTA, down to one a warp, where the step is small
+  int chunk = kChunk;
+  const int warps = threads_of(bits8) / 32;
+  while (chunk > warps && blocks / chunk < 8 * device_sm_count()) chunk >>= 1;
   tab.chunk_blocks = chunk;
   uint64_t chunks = 0;
   for (int i = 0; i < n; ++i) {
@@ -447,9 +459,9 @@ int launch(const moe_adamw_tensor *t, int n, bool bits8, const Hyper &H, cudaStr
   tab.chunk0[n] = (uint32_t)chunks;
   if (chunks == 0) return MOE_OK;
   if (bits8)
-    adamw_kernel<kMax, true><<<(unsigned)chunks, kThreads, 0, st>>>(tab, H);
+    adamw_kernel<kMax, true><<<(unsigned)chunks, threads_of(true), 0, st>>>(tab, H);
   else
-    adamw_kernel<kMax, false><<<(unsigned)chunks, kThreads, 0, st>>>(tab, H);
+    adamw_kernel<kMax, false><<<(unsigned)chunks, threads_of(false), 0, st>>>(tab, H);
   return check_launch();
 }
 
@@ -464,7 +476,7 @@ int check_codes(int64_t n, const void *mc, const void *ms, const void *rc, const
   return MOE_OK;
 }
 unsigned codes_grid(int64_t n) {
-  const int64_t need = ((n + kBlock - 1) / kBlock + kWarps - 1) / kWarps;
+  const int64_t need = ((n + kBlock - 1) / kBlock + kCodesThreads / 32 - 1) / (kCodesThreads / 32);
   const int64_t most = (int64_t)device_sm_count() * 8;
   return (unsigned)(need < most ? need : most);
 }
@@ -522,7 +534,7 @@ extern "C" int moe_adamw_decode(int64_t n, const void *m_code, const float *m_sc
                                 void *stream) {
   const int rc = check_codes(n, m_code, m_scale, r_code, r_scale, m, v);
   if (rc != MOE_OK || n == 0) return rc;
-  codes_kernel<false><<<codes_grid(n), kThreads, 0, as_stream(stream)>>>(
+  codes_kernel<false><<<codes_grid(n), kCodesThreads, 0, as_stream(stream)>>>(
       n, static_cast<uint8_t *>(const_cast<void *>(m_code)), const_cast<float *>(m_scale),
       static_cast<uint8_t *>(const_cast<void *>(r_code)), const_cast<float *>(r_scale), m, v);
   return check_launch();
@@ -532,7 +544,7 @@ extern "C" int moe_adamw_encode(int64_t n, const float *m, const float *v, void 
                                 float *m_scale, void *r_code, float *r_scale, void *stream) {
   const int rc = check_codes(n, m_code, m_scale, r_code, r_scale, m, v);
   if (rc != MOE_OK || n == 0) return rc;
-  codes_kernel<true><<<codes_grid(n), kThreads, 0, as_stream(stream)>>>(
+  codes_kernel<true><<<codes_grid(n), kCodesThreads, 0, as_stream(stream)>>>(
       n, static_cast<uint8_t *>(m_code), m_scale, static_cast<uint8_t *>(r_code), r_scale,
       const_cast<float *>(m), const_cast<float *>(v));
   return check_launch();
