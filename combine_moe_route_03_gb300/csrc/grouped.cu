@@ -11,25 +11,42 @@
 // 128 or 256 on M, and an expert of 270 rows would else pay for 384 or 512.
 //
 // CTA pairs (two SMs of a TPC): cta_group::2 MMAs of 256 x N x 16, N <= 256, binary32
-// accumulators in tensor memory.  Each CTA holds 128 of the tile's p and half of its q, so
-// a 64-deep block of t moves 32 KB into each SM for 512 tensor cycles at N = 256.
-//   warp 0  producer: TMA tiles into a ring of 6 stages (64 deep in t, 128-byte swizzle).
-//           An operand whose contiguous index is t (forward: both; trans: Q) is K-major,
-//           the others are MN-major in 64-wide column blocks: no operand is transposed by
-//           anyone.  The weights' map has the expert as a dimension, so tiles that pass
-//           an expert's edge in p or t read zeros, not the next expert.
+// accumulators in tensor memory.  Each CTA holds 128 of the tile's p and half of its q: a
+// 64-deep block of t moves 32 KB into each SM for 512 tensor cycles at N = 256.  A unit of
+// work is one expert, 256 p and up to 256 q (one accumulator; the other takes the next
+// unit's MMAs while this one's is stored) or 512 (both: the P tile is read once for the two,
+// 48 KB a block for 1024 cycles).  Units that share weights run side by side on the 76 pairs.
+//   warp 0  producer: TMA tiles into a ring in shared memory (128-byte swizzle).  An operand
+//           whose contiguous index is t (forward: both; trans: Q) is K-major, the others are
+//           MN-major in 64-wide column blocks: nothing is transposed by anyone.  The
+//           weights' map has the expert as a dimension, so tiles that pass an expert's edge
+//           in p or t read zeros, not the next expert.
 //   warp 1  MMA issuer (of the even CTA) and TMEM owner.
 //   warp 2  scheduler: decodes units from the table of segments, ahead of the others.
 //   warp 3  gradient only: t runs over rows, and the block after a segment's last row
 //           holds the next segment's (or padding: anything, NaN too).  MMAs take 16 rows
 //           at a time, so at most 15 rows must not count; this warp writes zeros over them
-//           in both operands before the MMA sees the stage.
-//   warps 4-11  epilogue: TMEM -> registers -> global, two accumulators in turn, so a
-//           unit's MMAs run beside the previous unit's stores.
+//           in both operands before the MMAs may read the block.
+//   warps 4-11  epilogue: TMEM -> registers -> global.  Forward and trans store the rows
+//           from registers, which leaves the ring 212 KB; the gradient, whose units are
+//           short and bound by their stores, hands blocks of 32 x 32 to bulk copies.
 // The tensor core's binary32 accumulation truncates: the relative error grows with the
 // number of additions (measured 1e-6 at t = 1024 and 1.9e-5 at 16384).  16-bit outputs
 // round far above that; binary32 gradients take partial sums of 512 rows and add them in
 // the epilogue's registers with rounding to nearest.
+//
+// What bounds it, and what it measured (64 experts, n = 4096, k = 7168; 6.76 TB/s and 1864
+// TFLOP/s are a copy's and a dense library product's rates):
+//   few rows an expert: the weights, once, from HBM (16 rows: 545 us, 6.9 TB/s).  By
+//     Little's law that takes the 130 KB and more of weights that the ring keeps under way
+//     in each SM; 64 KB gave 4.6 TB/s.
+//   about 256 rows, ragged: weights, rows and output from and to HBM, 676 us (6.1 TB/s).
+//   many rows: the tensor cores under the power cap, 1560 to 1960 TFLOP/s.
+//   gradient, 16 experts of about 256 rows: 214 us, 4.4 TB/s of writes; zeros alone are
+//     written at 6.9 TB/s, the MMAs alone would take 110 us.
+// Tried and not kept: requests into L2 ahead of the ring (560 -> 667 us, they queue before
+// the ring's own copies), Q multicast over clusters of two pairs (152 SMs hold 36 of them:
+// 5 % slower), 128-deep blocks for the gradient.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -42,7 +59,7 @@ namespace {
 constexpr int kFwd = 0, kTrans = 1, kGrad = 2;
 constexpr int kThreads = 384, kEpiWarps = 8;
 constexpr int BP = 256, BQ = 256, BT = 64;  // tile of a CTA pair, depth of a block of t
-constexpr int kWide = 2 * BQ;               // q's of a wide unit
+constexpr int kWide = 2 * BQ;               // q's of a unit with both accumulators
 constexpr int kUnitQ = 8;
 constexpr uint32_t kPBytes = 128 * BT * 2;  // a CTA's half of a P tile
 // Bytes of the operand ring, and of an epilogue warp's staging (gradient): a block of 32 x
@@ -202,7 +219,8 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 // The cluster's threads meet; nothing of their memory is ordered by it (a release would
-// first wait for every store).
+// first wait for every store).  What one CTA sends to the other's barriers has been waited
+// for there by then.
 __device__ __forceinline__ void cluster_meet() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
@@ -232,13 +250,11 @@ __device__ __forceinline__ void tma_add(const void *map, uint32_t src, int x, in
       : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// All of the thread's bulk stores but the last kBut have read their shared memory / all
-// are complete.
+// All of the thread's bulk stores but the last kBut have read their shared memory.
 template <int kBut>
 __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBut) : "memory");
 }
-__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -276,8 +292,10 @@ __device__ __forceinline__ void split_n(Unit &U, int step) {
     U.n[1] = (U.nq - U.n[0] + step - 1) / step * step;
   }
 }
-// The gradient's q's of a unit: 512 where the segment is long enough for the MMAs to
-// hide the stores of two accumulators, and sums are not kept in registers.
+// The gradient's q's of a unit: 512 where the segment is long enough that reading P once for
+// two accumulators is worth more than storing beside the next unit's MMAs (16 experts: 512
+// rows 372 us against 343 in units of 256, 768 rows the same, 1024 rows 578 against 589), and
+// sums are not kept in registers.
 template <bool kF32>
 __device__ __forceinline__ int grad_q(int nq, int count) {
   return !kF32 && nq > BQ && count >= kWideRows ? kWide : BQ;
@@ -479,147 +497,159 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     if (warp == 0) {
       if (elect_one()) {
-      // ---------------------------------------------------------- producer
-      const uint64_t pol_stream = policy_evict_first(), pol_keep = policy_evict_normal();
-      const uint32_t lead_full = mapa_shared(bar_full, 0);
-      Ring<kRing> ring;
-      uint32_t freed = 0;           // Ring::end of the last block that is known to be consumed,
-      int old_bar = 0, blocks = 0;  // the barriers of the next, and the blocks not known to be
-      uint32_t old_phase = 0;
-      for (int seq = 0;; ++seq) {
-        Unit U;
-        if (!take(seq, U)) break;
-        release_unit(seq);
-        if (U.end) break;
-        const uint64_t pol_p = U.once ? pol_stream : pol_keep;
-        const int half0 = U.n[0] / 2, half1 = U.n[1] / 2;
-        const int p0 = U.p0 + 128 * rank, qa = U.q0 + half0 * rank, qb = U.q0 + U.n[0] + half1 * rank;
-        constexpr int kUnitN = kQMn ? 64 : 16;
-        const CUtensorMap *map_a = &M.q[half0 / kUnitN - 1], *map_b = &M.q[half1 ? half1 / kUnitN - 1 : 0];
-        const uint32_t bytes = block_bytes(U.n[0], U.n[1]), to_b = kPBytes + half0 * (BT * 2);
-        const int z = kMode == kGrad ? 0 : U.z;
-        const int tail = kMode == kGrad && (U.rem & 15) ? U.blocks - 1 : -1;
-        int t = U.t0;
-        bool ok = true;
-        for (int b = 0; b < U.blocks; ++b, t += BT) {
-          const uint32_t dst = s_ring + ring.place(bytes);
-          while (ring.end - freed > kRing || blocks == kDepth) {
-            ok = wait(bar_empty + 8 * old_bar, old_phase, kWaitLimitNs);
-            if (!ok) break;
-            freed = *(volatile uint32_t *)&S.end[old_bar];
-            --blocks;
-            if (++old_bar == kDepth) {
-              old_bar = 0;
-              old_phase ^= 1;
-            }
-          }
-          if (!ok) break;
-          *(volatile uint32_t *)&S.end[ring.bar] = ring.end;
-          auto load = [&](auto counted_by_pair, uint32_t bar) {
-            constexpr bool kPair = decltype(counted_by_pair)::value;
-            auto tile = [&](uint32_t to, const CUtensorMap *map, int q, int half) {
-              if constexpr (!kQMn) {
-                tma_load<kPair>(to, map, bar, t, q, 0, 0, pol_keep);
-              } else if (P.q_blocked) {
-                tma_load<kPair>(to, map, bar, 0, t, q >> 6, 0, pol_keep);
-              } else {
-                for (int j = 0; j < half; j += 64)
-                  tma_load<kPair>(to + 128 * j, &M.q[0], bar, q + j, t, 0, 0, pol_keep);
+        // ---------------------------------------------------------- producer
+        const uint64_t pol_stream = policy_evict_first(), pol_keep = policy_evict_normal();
+        const uint32_t lead_full = mapa_shared(bar_full, 0);
+        Ring<kRing> ring;
+        uint32_t freed = 0;           // Ring::end of the last block that is known to be consumed,
+        int old_bar = 0, blocks = 0;  // the barriers of the next, and the blocks not known to be
+        uint32_t old_phase = 0;
+        for (int seq = 0;; ++seq) {
+          Unit U;
+          if (!take(seq, U)) break;
+          release_unit(seq);
+          if (U.end) break;
+          const uint64_t pol_p = U.once ? pol_stream : pol_keep;
+          const int half0 = U.n[0] / 2, half1 = U.n[1] / 2;
+          const int p0 = U.p0 + 128 * rank, qa = U.q0 + half0 * rank, qb = U.q0 + U.n[0] + half1 * rank;
+          constexpr int kUnitN = kQMn ? 64 : 16;
+          const CUtensorMap *map_a = &M.q[half0 / kUnitN - 1], *map_b = &M.q[half1 ? half1 / kUnitN - 1 : 0];
+          const uint32_t bytes = block_bytes(U.n[0], U.n[1]), to_b = kPBytes + half0 * (BT * 2);
+          const int z = kMode == kGrad ? 0 : U.z;
+          const int tail = kMode == kGrad && (U.rem & 15) ? U.blocks - 1 : -1;
+          int t = U.t0;
+          bool ok = true;
+          for (int b = 0; b < U.blocks; ++b, t += BT) {
+            const uint32_t dst = s_ring + ring.place(bytes);
+            while (ring.end - freed > kRing || blocks == kDepth) {
+              ok = wait(bar_empty + 8 * old_bar, old_phase, kWaitLimitNs);
+              if (!ok) break;
+              freed = *(volatile uint32_t *)&S.end[old_bar];
+              --blocks;
+              if (++old_bar == kDepth) {
+                old_bar = 0;
+                old_phase ^= 1;
               }
+            }
+            if (!ok) break;
+            *(volatile uint32_t *)&S.end[ring.bar] = ring.end;
+            auto load = [&](auto counted_by_pair, uint32_t bar) {
+              constexpr bool kPair = decltype(counted_by_pair)::value;
+              auto tile = [&](uint32_t to, const CUtensorMap *map, int q, int half) {
+                if constexpr (!kQMn) {
+                  tma_load<kPair>(to, map, bar, t, q, 0, 0, pol_keep);
+                } else if (P.q_blocked) {
+                  tma_load<kPair>(to, map, bar, 0, t, q >> 6, 0, pol_keep);
+                } else {
+                  for (int j = 0; j < half; j += 64)
+                    tma_load<kPair>(to + 128 * j, &M.q[0], bar, q + j, t, 0, 0, pol_keep);
+                }
+              };
+              if constexpr (kMode == kFwd) {
+                tma_load<kPair>(dst, &M.p, bar, t, p0, 0, z, pol_p);
+              } else if (P.p_blocked) {
+                tma_load<kPair>(dst, &M.p, bar, 0, t, p0 >> 6, z, pol_p);
+              } else {
+                tma_load<kPair>(dst, &M.p, bar, p0, t, 0, z, pol_p);
+                tma_load<kPair>(dst + 8192, &M.p, bar, p0 + 64, t, 0, z, pol_p);
+              }
+              tile(dst + kPBytes, map_a, qa, half0);
+              if (half1) tile(dst + to_b, map_b, qb, half1);
             };
-            if constexpr (kMode == kFwd) {
-              tma_load<kPair>(dst, &M.p, bar, t, p0, 0, z, pol_p);
-            } else if (P.p_blocked) {
-              tma_load<kPair>(dst, &M.p, bar, 0, t, p0 >> 6, z, pol_p);
+            if (kMode == kGrad && b == tail) {
+              // completes in this CTA, for its tail warp
+              mbar_arrive_expect_tx(bar_tail + 8 * ring.bar, bytes);
+              load(std::false_type{}, bar_tail + 8 * ring.bar);
             } else {
-              tma_load<kPair>(dst, &M.p, bar, p0, t, 0, z, pol_p);
-              tma_load<kPair>(dst + 8192, &M.p, bar, p0 + 64, t, 0, z, pol_p);
+              if (rank == 0)
+                mbar_arrive_expect_tx(bar_full + 8 * ring.bar, 2 * bytes);
+              else if (kMode == kGrad)
+                mbar_arrive_remote(lead_full + 8 * ring.bar);
+              load(std::true_type{}, lead_full + 8 * ring.bar);
             }
-            tile(dst + kPBytes, map_a, qa, half0);
-            if (half1) tile(dst + to_b, map_b, qb, half1);
-          };
-          if (kMode == kGrad && b == tail) {
-            // completes in this CTA, for its tail warp
-            mbar_arrive_expect_tx(bar_tail + 8 * ring.bar, bytes);
-            load(std::false_type{}, bar_tail + 8 * ring.bar);
-          } else {
-            if (rank == 0)
-              mbar_arrive_expect_tx(bar_full + 8 * ring.bar, 2 * bytes);
-            else if (kMode == kGrad)
-              mbar_arrive_remote(lead_full + 8 * ring.bar);
-            load(std::true_type{}, lead_full + 8 * ring.bar);
-          }
-          ++blocks;
-          ring.next_block();
-        }
-        if (!ok) break;
-      }
-      if (*abort) {  // let the copies in flight land before the CTA can exit
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 1000000ull) {
-        }
-      }
-      }
-    } else if (warp == 1) {
-      if (elect_one()) {
-      // -------------------------------------------------------- MMA issuer
-      // binary32 sums; A = P, B = Q, bits 15 / 16: MN-major
-      const uint32_t idesc0 = (1u << 4) | ((uint32_t)P.bf16 << 7) | ((uint32_t)P.bf16 << 10) |
-                              ((kPMn ? 1u : 0u) << 15) | ((kQMn ? 1u : 0u) << 16) |
-                              ((uint32_t)(BP >> 4) << 24);
-      int acc = 0;
-      Ring<kRing> ring;
-      bool ok = true;
-      Unit N;  // the next unit, taken while this one's last block is awaited
-      bool next = take(0, N);
-      for (int seq = 0; ok && next; ++seq) {
-        const Unit U = N;
-        release_unit(seq);
-        if (U.end) break;
-        if (rank != 0 || U.blocks == 0) next = take(seq + 1, N);
-        if (rank != 0) continue;  // the odd CTA only follows the unit stream
-        const int accs = U.n[1] ? 2 : 1, sums = sums_of(U);
-        const uint32_t bytes = block_bytes(U.n[0], U.n[1]);
-        const uint32_t idesc_a = idesc0 | ((uint32_t)(U.n[0] >> 3) << 17);
-        const uint32_t idesc_b = idesc0 | ((uint32_t)(U.n[1] >> 3) << 17);
-        const uint64_t to_b = U.n[0] / 2 * (BT * 2) / 16;  // from one Q tile to the other
-        for (int s = 0; s < sums && ok; ++s, acc += accs) {
-          for (int a = 0; a < accs && ok; ++a)
-            ok = wait(bar_acc_empty + 8 * ((acc + a) & 1), ((uint32_t)((acc + a) >> 1) & 1u) ^ 1u,
-                      kWaitLimitNs);
-          if (!ok) break;
-          tc_fence_after();
-          const int b0 = kF32 ? s * kSumBlocks : 0;
-          const int b1 = kF32 ? min(U.blocks, b0 + kSumBlocks) : U.blocks;
-          for (int b = b0; b < b1 && ok; ++b) {
-            if (b == U.blocks - 1) next = take(seq + 1, N);
-            ok = wait(bar_full + 8 * ring.bar, ring.phase, kWaitLimitNs);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t sp = s_ring + ring.place(bytes);
-            const uint64_t dp = operand_desc<kPMn>(sp);
-            uint64_t dq = operand_desc<kQMn>(sp + kPBytes);
-            const int steps = b == U.blocks - 1 ? (U.rem + 15) >> 4 : BT / 16;
-            for (int a = 0; a < accs; ++a) {
-              const uint32_t d = tmem + 256 * ((acc + a) & 1), idesc = a ? idesc_b : idesc_a;
-              mma_pair_f16(d, dp, dq, idesc, b != b0);
-              if (steps == BT / 16) {
-#pragma unroll
-                for (int j = 1; j < BT / 16; ++j)
-                  mma_pair_f16(d, dp + j * kStep<kPMn>, dq + j * kStep<kQMn>, idesc, 1);
-              } else {
-                for (int j = 1; j < steps; ++j)
-                  mma_pair_f16(d, dp + j * kStep<kPMn>, dq + j * kStep<kQMn>, idesc, 1);
-              }
-              dq += to_b;
-            }
-            tc_commit_pair_mc(bar_empty + 8 * ring.bar, kBoth);
+            ++blocks;
             ring.next_block();
           }
           if (!ok) break;
-          for (int a = 0; a < accs; ++a) tc_commit_pair_mc(bar_acc_full + 8 * ((acc + a) & 1), kBoth);
+        }
+        // what the MMAs' commits still have to say to this CTA's barriers comes before its end
+        for (bool ok = !*abort; ok && blocks > 0; --blocks) {
+          ok = wait(bar_empty + 8 * old_bar, old_phase, kWaitLimitNs);
+          if (++old_bar == kDepth) {
+            old_bar = 0;
+            old_phase ^= 1;
+          }
+        }
+        if (*abort) {  // let the copies in flight land before the CTA can exit
+          const uint64_t t0 = globaltimer();
+          while (globaltimer() - t0 < 1000000ull) {
+          }
         }
       }
+    } else if (warp == 1) {
+      if (elect_one()) {
+        // -------------------------------------------------------- MMA issuer
+        // binary32 sums; A = P, B = Q, bits 15 / 16: MN-major
+        const uint32_t idesc0 = (1u << 4) | ((uint32_t)P.bf16 << 7) | ((uint32_t)P.bf16 << 10) |
+                                ((kPMn ? 1u : 0u) << 15) | ((kQMn ? 1u : 0u) << 16) |
+                                ((uint32_t)(BP >> 4) << 24);
+        int acc = 0;
+        Ring<kRing> ring;
+        bool ok = true;
+        Unit N;  // the next unit, taken while this one's last block is awaited
+        bool next = take(0, N);
+        for (int seq = 0; ok && next; ++seq) {
+          const Unit U = N;
+          release_unit(seq);
+          if (U.end) break;
+          if (rank != 0 || U.blocks == 0) next = take(seq + 1, N);
+          if (rank != 0) continue;  // the odd CTA only follows the unit stream
+          const int accs = U.n[1] ? 2 : 1, sums = sums_of(U);
+          const uint32_t bytes = block_bytes(U.n[0], U.n[1]);
+          const uint32_t idesc_a = idesc0 | ((uint32_t)(U.n[0] >> 3) << 17);
+          const uint32_t idesc_b = idesc0 | ((uint32_t)(U.n[1] >> 3) << 17);
+          const uint64_t to_b = U.n[0] / 2 * (BT * 2) / 16;  // from one Q tile to the other
+          for (int s = 0; s < sums && ok; ++s, acc += accs) {
+            for (int a = 0; a < accs && ok; ++a)
+              ok = wait(bar_acc_empty + 8 * ((acc + a) & 1), ((uint32_t)((acc + a) >> 1) & 1u) ^ 1u,
+                        kWaitLimitNs);
+            if (!ok) break;
+            tc_fence_after();
+            const int b0 = kF32 ? s * kSumBlocks : 0;
+            const int b1 = kF32 ? min(U.blocks, b0 + kSumBlocks) : U.blocks;
+            for (int b = b0; b < b1 && ok; ++b) {
+              if (b == U.blocks - 1) next = take(seq + 1, N);
+              ok = wait(bar_full + 8 * ring.bar, ring.phase, kWaitLimitNs);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t sp = s_ring + ring.place(bytes);
+              const uint64_t dp = operand_desc<kPMn>(sp);
+              uint64_t dq = operand_desc<kQMn>(sp + kPBytes);
+              const int steps = b == U.blocks - 1 ? (U.rem + 15) >> 4 : BT / 16;
+              for (int a = 0; a < accs; ++a) {
+                const uint32_t d = tmem + 256 * ((acc + a) & 1), idesc = a ? idesc_b : idesc_a;
+                mma_pair_f16(d, dp, dq, idesc, b != b0);
+                if (steps == BT / 16) {
+#pragma unroll
+                  for (int j = 1; j < BT / 16; ++j)
+                    mma_pair_f16(d, dp + j * kStep<kPMn>, dq + j * kStep<kQMn>, idesc, 1);
+                } else {
+                  for (int j = 1; j < steps; ++j)
+                    mma_pair_f16(d, dp + j * kStep<kPMn>, dq + j * kStep<kQMn>, idesc, 1);
+                }
+                dq += to_b;
+              }
+              tc_commit_pair_mc(bar_empty + 8 * ring.bar, kBoth);
+              ring.next_block();
+            }
+            if (!ok) break;
+            for (int a = 0; a < accs; ++a) tc_commit_pair_mc(bar_acc_full + 8 * ((acc + a) & 1), kBoth);
+          }
+        }
+        // so do the odd CTA's last releases
+        if (rank == 0)
+          for (int a = max(0, acc - 2); ok && a < acc; ++a)
+            ok = wait(bar_acc_empty + 8 * (a & 1), (uint32_t)(a >> 1) & 1u, kWaitLimitNs);
       }
     } else if (warp == 2 && lane == 0) {
       // --------------------------------------------------------- scheduler
@@ -646,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // -------------------------------------- rows past the segment's last
       const uint32_t lead_full = mapa_shared(bar_full, 0);
       Ring<kRing> ring;
-      uint32_t parity = 0;  // of each tail and peer barrier
+      uint32_t parity = 0;  // of each tail barrier
       for (int seq = 0;; ++seq) {
         Unit U;
         if (!take_warp(seq, U)) break;
@@ -809,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (kMode == kGrad && elect_one()) bulk_wait();
+    if (kMode == kGrad && elect_one()) bulk_wait_read<0>();
   }
 
   tc_fence_before();
