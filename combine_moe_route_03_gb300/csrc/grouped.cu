@@ -768,7 +768,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         // 16 q's x 32 p at a time through the warp's two staging blocks; with accumulate the
-        // copy adds to the output in L2 (each value once, so in no particular order)
+        // copy adds to the output in L2 (each value once, so in no particular order).  A block
+        // is written only if its copy follows: the wait counts copies.
+        if (pw >= P.np) continue;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int c = 32 * (half + 2 * g);
@@ -782,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int j = 0; j < 16; ++j) row[32 * j] = sum[g][16 * h + j];
               fence_async_shared();
               __syncwarp();
-              if (pw < P.np && elect_one()) {
+              if (elect_one()) {
                 if (P.accumulate)
                   tma_add(&M.out, stage0 + turn, pw, U.q0 + c + 16 * h, U.z);
                 else

@@ -475,6 +475,7 @@ int moe_combine(const moe_combine_cfg *cfg, const void *Y, const int32_t *row_of
  * What the device finds wrong is bounded, not followed: a negative count counts as 0 and
  * sets MOE_STATUS_BAD_INDEX; a segment that passes `rows` is cut there, and a count
  * above cap cut to it, and both set MOE_STATUS_CAPACITY.
+ * The status words of these entry points are nullable.
  * Limits: 1 <= E <= 1024, align >= 1, cap >= 0, 0 <= rows <= 2^31 - 1 - 1024.
  */
 typedef struct moe_segments {
@@ -520,6 +521,7 @@ int moe_grouped_gemm(const moe_ggemm_args *args, void *stream);
  *   With MOE_TYPE_F32 partial sums of at most 512 rows are joined by binary32 additions
  *   (the tensor core's own accumulation truncates, which would show over long segments).
  *   The order of the additions is fixed: the same inputs give the same bits.
+ *   (accumulate adds where the gradient lies, in the L2, one addition an element.)
  * Limits and errors as moe_grouped_gemm; a bad out_type, or accumulate without
  * MOE_TYPE_F32: MOE_ERR_INVALID.
  */
@@ -546,9 +548,10 @@ int moe_grouped_wgrad(const moe_wgrad_args *args, void *stream);
  *     and, with drow_w non-NULL, drow_w[r] = sum_j dh a u (the gradient of w[r]),
  *     for dh [rows][I] the gradient of the activation.
  * Computed in binary32, rounded once.  drow_w is summed in a fixed order.  The
- * backward's out may be gu itself.  I >= 1; any alignment of the element type (16-byte aligned tensors with
- * I % 8 == 0 take the fast path).  Errors: MOE_ERR_INVALID for a null pointer, a bad
- * type or size; MOE_ERR_UNSUPPORTED outside the limits of the segments, or I > 2^24.
+ * backward's out may be gu itself.  I >= 1; any alignment of the element type (16-byte
+ * aligned tensors with I % 8 == 0 take the fast path).  Errors: MOE_ERR_INVALID for a
+ * null pointer, a bad type or size; MOE_ERR_UNSUPPORTED outside the limits of the
+ * segments, or I > 2^24.
  */
 typedef struct moe_swiglu_args {
   moe_segments seg;
@@ -583,7 +586,8 @@ int moe_swiglu_backward(const moe_swiglu_args *args, void *stream);
  *   2 / L for the largest values and reaches down to 1e-5 of them.  A block whose
  *   largest value is below 2^-126 is held as zeros; a NaN in a block makes its scale NaN.
  *   m_code int8 [n], r_code uint8 [n], m_scale and r_scale float [ceil(n / 256)].
- * The update of p uses the new moments before they are rounded to codes.
+ * The update of p uses the new moments before they are rounded to codes; its root and
+ * quotient are the device's approximate ones (a few 2^-23 of the step).
  * `tensors` is a host array.  A tensor's pointers need the alignment of their element;
  * 16-byte aligned ones take the fast path.  Errors, before any launch: MOE_ERR_INVALID
  * for a null pointer, n < 0, a bad type, state_bits, step < 1, betas outside [0, 1), eps

@@ -653,3 +653,34 @@ def test_operators_in_a_captured_graph(dev):
     torch.cuda.synchronize()
     want = api.grouped_gemm(x, w, counts)
     assert torch.equal(out, want) and torch.equal(h, api.swiglu(want, counts=counts))
+
+
+@pytest.mark.parametrize("counts", [[45, 274, 115, 60, 50, 35], [9, 0, 900, 1300]])
+@pytest.mark.parametrize("n,k", [(5792, 1984), (1232, 672), (4288, 376)])
+def test_many_units_a_pair_with_partial_tiles_between(dev, counts, n, k):
+    """Each CTA pair works through several tiles, whole ones and ones that pass the extents
+    by turns, back to back.  Whole numbers whose sums binary32 holds: equality, whatever the
+    order of the additions."""
+    gen = torch.Generator("cuda").manual_seed(11)
+    rows = sum(counts)
+
+    def whole(*shape):
+        return torch.randint(-3, 4, shape, generator=gen, device="cuda").to(BF16)
+
+    x, dy, w, c = whole(rows, k), whole(rows, n), whole(len(counts), n, k), i32(counts)
+    base = torch.randint(-9, 10, w.shape, generator=gen, device="cuda").to(F32)
+    y, dx, dw = [], [], []
+    for e, (start, m) in enumerate(zip(starts_of(counts), counts)):
+        xe, dye = x[start:start + m].double(), dy[start:start + m].double()
+        y.append(xe @ w[e].double().t())
+        dx.append(dye @ w[e].double())
+        dw.append((dye.t() @ xe).to(F32))
+    y, dx, dw = torch.cat(y).to(F32).to(BF16), torch.cat(dx).to(F32).to(BF16), torch.stack(dw)
+    acc = base.clone()
+    for turn in range(3):
+        assert torch.equal(api.grouped_gemm(x, w, c), y)
+        assert torch.equal(api.grouped_gemm(dy, w, c, trans=True), dx)
+        assert torch.equal(api.grouped_wgrad(dy, x, c), dw.to(BF16))
+        assert torch.equal(api.grouped_wgrad(dy, x, c, out_dtype=F32), dw)
+        api.grouped_wgrad(dy, x, c, out=acc, accumulate=True)
+        assert torch.equal(acc, base + (turn + 1) * dw)
