@@ -49,6 +49,7 @@
 // 5 % slower), 128-deep blocks for the gradient.
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "segments.cuh"
@@ -68,7 +69,13 @@ constexpr uint32_t kStage = 2048;
 constexpr uint32_t ring_bytes(int mode, bool f32) { return (mode != kGrad ? 212 : f32 ? 180 : 196) * 1024; }
 constexpr uint32_t stage_bytes(int mode, bool f32) { return mode != kGrad ? 0 : f32 ? 2 * kStage : kStage; }
 constexpr int kSumBlocks = 8;  // blocks of one partial sum (binary32 output): 512 rows
-constexpr int kWideRows = 896;  // rows from which the gradient takes wide units
+// Slots of the gradient's operands, 16 KB each: P tiles stay while several Q tiles pass.  A Q
+// slot's barriers serve a P tile too where one comes along.  Every use of a P tile has a Q tile
+// of its own, so by the time that the Q slot of a block is free again, so is a P slot loaded
+// as many P tiles ago as there are Q slots, or more.
+constexpr int kPSlots = 6;
+constexpr int q_slots(bool f32) { return (int)(ring_bytes(2, f32) / (16 * 1024)) - kPSlots; }
+static_assert(q_slots(false) <= kPSlots && q_slots(true) <= kPSlots, "P slots are reused by Q's barriers");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -80,8 +87,9 @@ struct Unit {
   int z;      // expert
   int p0;     // first p of the pair's tile
   int q0;     // first q: a row of the buffer (forward, trans), a column of dy (gradient)
-  int nq;     // q's that exist, at most 512
+  int nq;     // q's that exist, at most 512 (gradient: of all its Q tiles)
   int n[2];   // N of the MMAs of each accumulator (n[1] 0: one accumulator)
+  int tiles, chunk; // gradient: Q tiles, and the blocks of t that each takes at a time
   int t0;     // first t: 0, or the segment's first row (gradient)
   int blocks; // 64-deep blocks of t
   int rem;    // t's of the last block, 1..64
@@ -119,6 +127,19 @@ struct Ring {
   }
 };
 
+// The gradient's slots of one operand, in turn.
+template <int kSlots>
+struct Slots {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == kSlots) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 struct Shared {
   uint64_t full[kDepth], empty[kDepth], tail[kDepth];
   uint64_t acc_full[2], acc_empty[2];
@@ -150,6 +171,7 @@ struct GroupedParams {
   SegParams seg;
   int np, nq, nt;  // extents of p; of q (gradient: n); of t (forward, trans)
   int p_blocked, q_blocked;
+  int group;  // gradient: most Q tiles of a unit
   int bf16;
   int accumulate;
   void *out;
@@ -282,24 +304,34 @@ __device__ __forceinline__ int row_tiles(int count) {
   const int rows = tile_rows(count);
   return (count + rows - 1) / rows;
 }
-// N of each accumulator for nq q's, in multiples of `step`.
-__device__ __forceinline__ void split_n(Unit &U, int step) {
+// N of each accumulator for nq q's.
+__device__ __forceinline__ void split_n(Unit &U) {
   if (U.nq <= BQ) {
-    U.n[0] = (U.nq + step - 1) / step * step;
+    U.n[0] = (U.nq + 31) / 32 * 32;
     U.n[1] = 0;
   } else {
-    U.n[0] = ((U.nq + 1) / 2 + step - 1) / step * step;
-    U.n[1] = (U.nq - U.n[0] + step - 1) / step * step;
+    U.n[0] = ((U.nq + 1) / 2 + 31) / 32 * 32;
+    U.n[1] = (U.nq - U.n[0] + 31) / 32 * 32;
   }
 }
-// The gradient's q's of a unit: 512 where the segment is long enough that reading P once for
-// two accumulators is worth more than storing beside the next unit's MMAs (16 experts: 512
-// rows 372 us against 343 in units of 256, 768 rows the same, 1024 rows 578 against 589), and
-// sums are not kept in registers.
+// The gradient's Q tiles of a unit.  A short segment's P tiles all stay in their slots: one
+// Q tile after the other passes over them (chunk: every block), with as many Q tiles as the
+// host allows.  A long segment's pass in chunks, each Q tile in its own accumulator, so two.
+// Either way each P tile is read once for all of them, and an accumulator is stored beside the
+// MMAs of the other.  Long sums in registers leave room for one Q tile.
 template <bool kF32>
-__device__ __forceinline__ int grad_q(int nq, int count) {
-  return !kF32 && nq > BQ && count >= kWideRows ? kWide : BQ;
+__device__ __forceinline__ int grad_tiles(int group, int count) {
+  return count <= kPSlots * BT ? group : kF32 ? 1 : min(group, 2);
 }
+template <bool kF32>
+__device__ __forceinline__ int grad_chunk(int blocks) {
+  if (blocks <= kPSlots) return max(blocks, 1);
+  if (kF32) return kSumBlocks;
+  const int chunks = (blocks + kPSlots - 1) / kPSlots;
+  return (blocks + chunks - 1) / chunks;
+}
+// N of the MMAs of Q tile g: whole 64-wide column blocks in each CTA.
+__device__ __forceinline__ int grad_n(int nq, int g) { return nq - BQ * g > BQ / 2 ? BQ : BQ / 2; }
 
 // Unit u: the segments in order, within one the p tiles, within one the row tiles (or, for
 // the gradient, the q tiles), so units that share a weight tile run side by side.  e: the
@@ -315,18 +347,19 @@ __device__ __forceinline__ Unit get_unit(const GroupedParams &P, const SegTable 
   U.z = e;
   U.p0 = pt * BP;
   if constexpr (kMode == kGrad) {
-    const int q = grad_q<kF32>(P.nq, count);
+    const int q = grad_tiles<kF32>(P.group, count) * BQ;
     U.q0 = qt * q;
     U.nq = min(q, P.nq - U.q0);
-    split_n(U, 128);  // whole 64-wide column blocks in each CTA
+    U.tiles = (U.nq + BQ - 1) / BQ;
     U.t0 = T.start[e];
     U.blocks = (count + BT - 1) / BT;
     U.rem = count - (U.blocks - 1) * BT;
+    U.chunk = grad_chunk<kF32>(U.blocks);
   } else {
     const int rows = tile_rows(count);
     U.q0 = T.start[e] + qt * rows;
     U.nq = min(rows, count - qt * rows);
-    split_n(U, 32);
+    split_n(U);
     U.blocks = (P.nt + BT - 1) / BT;
     U.rem = P.nt - (U.blocks - 1) * BT;
     U.once = tiles == 1;
@@ -401,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kF32 = sizeof(O) == 4;
   constexpr uint32_t kRing = ring_bytes(kMode, kF32);
   constexpr bool kPMn = kMode != kFwd, kQMn = kMode == kGrad;
+  constexpr int kQSlots = q_slots(kF32);
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -445,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       P.seg, S.table, S.part,
       [&](int n) {
         if constexpr (kMode == kGrad) {
-          const int q = grad_q<kF32>(P.nq, n);
+          const int q = grad_tiles<kF32>(P.group, n) * BQ;
           return P.accumulate && n == 0 ? 0 : (P.nq + q - 1) / q;
         }
         return row_tiles(n);
@@ -489,10 +523,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
   auto release_unit = [&](int seq) { mbar_arrive(bar_unit_empty + 8 * (seq % kUnitQ)); };
-  // Blocks of one accumulation: all of the unit's, or (binary32 output) kSumBlocks.
-  auto sums_of = [](const Unit &U) {
-    return kF32 ? max(1, (U.blocks + kSumBlocks - 1) / kSumBlocks) : 1;
-  };
 
   if (warp < 4) {
     if (warp == 0) {
@@ -500,84 +530,119 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------------------------------------------------- producer
         const uint64_t pol_stream = policy_evict_first(), pol_keep = policy_evict_normal();
         const uint32_t lead_full = mapa_shared(bar_full, 0);
-        Ring<kRing> ring;
-        uint32_t freed = 0;           // Ring::end of the last block that is known to be consumed,
-        int old_bar = 0, blocks = 0;  // the barriers of the next, and the blocks not known to be
-        uint32_t old_phase = 0;
-        for (int seq = 0;; ++seq) {
-          Unit U;
-          if (!take(seq, U)) break;
-          release_unit(seq);
-          if (U.end) break;
-          const uint64_t pol_p = U.once ? pol_stream : pol_keep;
-          const int half0 = U.n[0] / 2, half1 = U.n[1] / 2;
-          const int p0 = U.p0 + 128 * rank, qa = U.q0 + half0 * rank, qb = U.q0 + U.n[0] + half1 * rank;
-          constexpr int kUnitN = kQMn ? 64 : 16;
-          const CUtensorMap *map_a = &M.q[half0 / kUnitN - 1], *map_b = &M.q[half1 ? half1 / kUnitN - 1 : 0];
-          const uint32_t bytes = block_bytes(U.n[0], U.n[1]), to_b = kPBytes + half0 * (BT * 2);
-          const int z = kMode == kGrad ? 0 : U.z;
-          const int tail = kMode == kGrad && (U.rem & 15) ? U.blocks - 1 : -1;
-          int t = U.t0;
+        if constexpr (kMode == kGrad) {
+          int ps = 0;
+          Slots<kQSlots> qs;
           bool ok = true;
-          for (int b = 0; b < U.blocks; ++b, t += BT) {
-            const uint32_t dst = s_ring + ring.place(bytes);
-            while (ring.end - freed > kRing || blocks == kDepth) {
-              ok = wait(bar_empty + 8 * old_bar, old_phase, kWaitLimitNs);
-              if (!ok) break;
-              freed = *(volatile uint32_t *)&S.end[old_bar];
-              --blocks;
-              if (++old_bar == kDepth) {
-                old_bar = 0;
-                old_phase ^= 1;
+          for (int seq = 0; ok; ++seq) {
+            Unit U;
+            if (!take(seq, U)) break;
+            release_unit(seq);
+            if (U.end) break;
+            const int p0 = U.p0 + 128 * rank;
+            const int tail = (U.rem & 15) ? U.blocks - 1 : -1;
+            for (int b0 = 0; ok && b0 < U.blocks; b0 += U.chunk) {
+              const int b1 = min(U.blocks, b0 + U.chunk);
+              for (int g = 0; ok && g < U.tiles; ++g) {
+                const int half = grad_n(U.nq, g) / 2, q0 = U.q0 + BQ * g + half * rank;
+                const uint32_t bytes = half * (BT * 2) + (g == 0 ? kPBytes : 0);
+                int t = U.t0 + b0 * BT;
+                for (int b = b0; b < b1; ++b, t += BT, qs.next()) {
+                  ok = wait(bar_empty + 8 * qs.at, qs.phase ^ 1u, kWaitLimitNs);
+                  if (!ok) break;
+                  const uint32_t to_p = s_ring + ps * kPBytes, to_q = s_ring + (kPSlots + qs.at) * kPBytes;
+                  auto load = [&](auto counted_by_pair, uint32_t bar) {
+                    constexpr bool kPair = decltype(counted_by_pair)::value;
+                    if (g == 0) {
+                      if (P.p_blocked) {
+                        tma_load<kPair>(to_p, &M.p, bar, 0, t, p0 >> 6, 0, pol_keep);
+                      } else {
+                        tma_load<kPair>(to_p, &M.p, bar, p0, t, 0, 0, pol_keep);
+                        tma_load<kPair>(to_p + 8192, &M.p, bar, p0 + 64, t, 0, 0, pol_keep);
+                      }
+                    }
+                    if (P.q_blocked) {
+                      tma_load<kPair>(to_q, &M.q[half / 64 - 1], bar, 0, t, q0 >> 6, 0, pol_keep);
+                    } else {
+                      for (int j = 0; j < half; j += 64)
+                        tma_load<kPair>(to_q + 128 * j, &M.q[0], bar, q0 + j, t, 0, 0, pol_keep);
+                    }
+                  };
+                  if (b == tail) {
+                    // completes in this CTA, for its tail warp
+                    mbar_arrive_expect_tx(bar_tail + 8 * qs.at, bytes);
+                    load(std::false_type{}, bar_tail + 8 * qs.at);
+                  } else {
+                    if (rank == 0)
+                      mbar_arrive_expect_tx(bar_full + 8 * qs.at, 2 * bytes);
+                    else
+                      mbar_arrive_remote(lead_full + 8 * qs.at);
+                    load(std::true_type{}, lead_full + 8 * qs.at);
+                  }
+                  if (g == 0 && ++ps == kPSlots) ps = 0;
+                }
               }
+            }
+          }
+          // what the MMAs' commits still have to say to this CTA's barriers comes before its end
+          ok = ok && !*abort;
+          for (int i = 0; ok && i < kQSlots; ++i, qs.next())
+            ok = wait(bar_empty + 8 * qs.at, qs.phase ^ 1u, kWaitLimitNs);
+        } else {
+          Ring<kRing> ring;
+          uint32_t freed = 0;           // Ring::end of the last block that is known to be consumed,
+          int old_bar = 0, blocks = 0;  // the barriers of the next, and the blocks not known to be
+          uint32_t old_phase = 0;
+          for (int seq = 0;; ++seq) {
+            Unit U;
+            if (!take(seq, U)) break;
+            release_unit(seq);
+            if (U.end) break;
+            const uint64_t pol_p = U.once ? pol_stream : pol_keep;
+            const int half0 = U.n[0] / 2, half1 = U.n[1] / 2;
+            const int p0 = U.p0 + 128 * rank, qa = U.q0 + half0 * rank, qb = U.q0 + U.n[0] + half1 * rank;
+            const CUtensorMap *map_a = &M.q[half0 / 16 - 1], *map_b = &M.q[half1 ? half1 / 16 - 1 : 0];
+            const uint32_t bytes = block_bytes(U.n[0], U.n[1]), to_b = kPBytes + half0 * (BT * 2);
+            int t = 0;
+            bool ok = true;
+            for (int b = 0; b < U.blocks; ++b, t += BT) {
+              const uint32_t dst = s_ring + ring.place(bytes);
+              while (ring.end - freed > kRing || blocks == kDepth) {
+                ok = wait(bar_empty + 8 * old_bar, old_phase, kWaitLimitNs);
+                if (!ok) break;
+                freed = *(volatile uint32_t *)&S.end[old_bar];
+                --blocks;
+                if (++old_bar == kDepth) {
+                  old_bar = 0;
+                  old_phase ^= 1;
+                }
+              }
+              if (!ok) break;
+              *(volatile uint32_t *)&S.end[ring.bar] = ring.end;
+              const uint32_t bar = lead_full + 8 * ring.bar;
+              if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * ring.bar, 2 * bytes);
+              if constexpr (kMode == kFwd) {
+                tma_load<true>(dst, &M.p, bar, t, p0, 0, U.z, pol_p);
+              } else if (P.p_blocked) {
+                tma_load<true>(dst, &M.p, bar, 0, t, p0 >> 6, U.z, pol_p);
+              } else {
+                tma_load<true>(dst, &M.p, bar, p0, t, 0, U.z, pol_p);
+                tma_load<true>(dst + 8192, &M.p, bar, p0 + 64, t, 0, U.z, pol_p);
+              }
+              tma_load<true>(dst + kPBytes, map_a, bar, t, qa, 0, 0, pol_keep);
+              if (half1) tma_load<true>(dst + to_b, map_b, bar, t, qb, 0, 0, pol_keep);
+              ++blocks;
+              ring.next_block();
             }
             if (!ok) break;
-            *(volatile uint32_t *)&S.end[ring.bar] = ring.end;
-            auto load = [&](auto counted_by_pair, uint32_t bar) {
-              constexpr bool kPair = decltype(counted_by_pair)::value;
-              auto tile = [&](uint32_t to, const CUtensorMap *map, int q, int half) {
-                if constexpr (!kQMn) {
-                  tma_load<kPair>(to, map, bar, t, q, 0, 0, pol_keep);
-                } else if (P.q_blocked) {
-                  tma_load<kPair>(to, map, bar, 0, t, q >> 6, 0, pol_keep);
-                } else {
-                  for (int j = 0; j < half; j += 64)
-                    tma_load<kPair>(to + 128 * j, &M.q[0], bar, q + j, t, 0, 0, pol_keep);
-                }
-              };
-              if constexpr (kMode == kFwd) {
-                tma_load<kPair>(dst, &M.p, bar, t, p0, 0, z, pol_p);
-              } else if (P.p_blocked) {
-                tma_load<kPair>(dst, &M.p, bar, 0, t, p0 >> 6, z, pol_p);
-              } else {
-                tma_load<kPair>(dst, &M.p, bar, p0, t, 0, z, pol_p);
-                tma_load<kPair>(dst + 8192, &M.p, bar, p0 + 64, t, 0, z, pol_p);
-              }
-              tile(dst + kPBytes, map_a, qa, half0);
-              if (half1) tile(dst + to_b, map_b, qb, half1);
-            };
-            if (kMode == kGrad && b == tail) {
-              // completes in this CTA, for its tail warp
-              mbar_arrive_expect_tx(bar_tail + 8 * ring.bar, bytes);
-              load(std::false_type{}, bar_tail + 8 * ring.bar);
-            } else {
-              if (rank == 0)
-                mbar_arrive_expect_tx(bar_full + 8 * ring.bar, 2 * bytes);
-              else if (kMode == kGrad)
-                mbar_arrive_remote(lead_full + 8 * ring.bar);
-              load(std::true_type{}, lead_full + 8 * ring.bar);
-            }
-            ++blocks;
-            ring.next_block();
           }
-          if (!ok) break;
-        }
-        // what the MMAs' commits still have to say to this CTA's barriers comes before its end
-        for (bool ok = !*abort; ok && blocks > 0; --blocks) {
-          ok = wait(bar_empty + 8 * old_bar, old_phase, kWaitLimitNs);
-          if (++old_bar == kDepth) {
-            old_bar = 0;
-            old_phase ^= 1;
+          // what the MMAs' commits still have to say to this CTA's barriers comes before its end
+          for (bool ok = !*abort; ok && blocks > 0; --blocks) {
+            ok = wait(bar_empty + 8 * old_bar, old_phase, kWaitLimitNs);
+            if (++old_bar == kDepth) {
+              old_bar = 0;
+              old_phase ^= 1;
+            }
           }
         }
         if (*abort) {  // let the copies in flight land before the CTA can exit
@@ -594,56 +659,95 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 ((kPMn ? 1u : 0u) << 15) | ((kQMn ? 1u : 0u) << 16) |
                                 ((uint32_t)(BP >> 4) << 24);
         int acc = 0;
-        Ring<kRing> ring;
         bool ok = true;
-        Unit N;  // the next unit, taken while this one's last block is awaited
-        bool next = take(0, N);
-        for (int seq = 0; ok && next; ++seq) {
-          const Unit U = N;
-          release_unit(seq);
-          if (U.end) break;
-          if (rank != 0 || U.blocks == 0) next = take(seq + 1, N);
-          if (rank != 0) continue;  // the odd CTA only follows the unit stream
-          const int accs = U.n[1] ? 2 : 1, sums = sums_of(U);
-          const uint32_t bytes = block_bytes(U.n[0], U.n[1]);
-          const uint32_t idesc_a = idesc0 | ((uint32_t)(U.n[0] >> 3) << 17);
-          const uint32_t idesc_b = idesc0 | ((uint32_t)(U.n[1] >> 3) << 17);
-          const uint64_t to_b = U.n[0] / 2 * (BT * 2) / 16;  // from one Q tile to the other
-          for (int s = 0; s < sums && ok; ++s, acc += accs) {
+        // 64-deep blocks, the last one in steps of 16; the accumulator d starts anew at the first
+        auto multiply = [&](uint32_t d, uint64_t dp, uint64_t dq, uint32_t idesc, int steps, bool more) {
+          mma_pair_f16(d, dp, dq, idesc, more);
+          if (steps == BT / 16) {
+#pragma unroll
+            for (int j = 1; j < BT / 16; ++j)
+              mma_pair_f16(d, dp + j * kStep<kPMn>, dq + j * kStep<kQMn>, idesc, 1);
+          } else {
+            for (int j = 1; j < steps; ++j)
+              mma_pair_f16(d, dp + j * kStep<kPMn>, dq + j * kStep<kQMn>, idesc, 1);
+          }
+        };
+        if constexpr (kMode == kGrad) {
+          int ps = 0;
+          Slots<kQSlots> qs;
+          for (int seq = 0; ok; ++seq) {
+            Unit U;
+            if (!take(seq, U)) break;
+            release_unit(seq);
+            if (U.end) break;
+            if (rank != 0) continue;  // the odd CTA only follows the unit stream
+            for (int b0 = 0; ok && b0 < U.blocks; b0 += U.chunk) {
+              const int b1 = min(U.blocks, b0 + U.chunk), first = ps;
+              ps = (ps + b1 - b0) % kPSlots;
+              for (int g = 0; ok && g < U.tiles; ++g) {
+                const int a = kF32 ? acc : acc + g;
+                const bool fresh = kF32 || b0 == 0;
+                if (fresh) {
+                  ok = wait(bar_acc_empty + 8 * (a & 1), ((uint32_t)(a >> 1) & 1u) ^ 1u, kWaitLimitNs);
+                  if (!ok) break;
+                  tc_fence_after();
+                }
+                const uint32_t idesc = idesc0 | ((uint32_t)(grad_n(U.nq, g) >> 3) << 17);
+                int at = first;
+                for (int b = b0; b < b1; ++b) {
+                  ok = wait(bar_full + 8 * qs.at, qs.phase, kWaitLimitNs);
+                  if (!ok) break;
+                  tc_fence_after();
+                  multiply(tmem + 256 * (a & 1), operand_desc<kPMn>(s_ring + at * kPBytes),
+                           operand_desc<kQMn>(s_ring + (kPSlots + qs.at) * kPBytes), idesc,
+                           b == U.blocks - 1 ? (U.rem + 15) >> 4 : BT / 16, !fresh || b != b0);
+                  tc_commit_pair_mc(bar_empty + 8 * qs.at, kBoth);
+                  qs.next();
+                  if (++at == kPSlots) at = 0;
+                }
+                if (ok && (kF32 || b1 == U.blocks)) tc_commit_pair_mc(bar_acc_full + 8 * (a & 1), kBoth);
+                if (kF32) ++acc;
+              }
+            }
+            if (!kF32 && U.blocks > 0) acc += U.tiles;
+          }
+        } else {
+          Ring<kRing> ring;
+          Unit N;  // the next unit, taken while this one's last block is awaited
+          bool next = take(0, N);
+          for (int seq = 0; ok && next; ++seq) {
+            const Unit U = N;
+            release_unit(seq);
+            if (U.end) break;
+            if (rank != 0) {  // the odd CTA only follows the unit stream
+              next = take(seq + 1, N);
+              continue;
+            }
+            const int accs = U.n[1] ? 2 : 1;
+            const uint32_t bytes = block_bytes(U.n[0], U.n[1]);
+            const uint32_t idesc_a = idesc0 | ((uint32_t)(U.n[0] >> 3) << 17);
+            const uint32_t idesc_b = idesc0 | ((uint32_t)(U.n[1] >> 3) << 17);
+            const uint64_t to_b = U.n[0] / 2 * (BT * 2) / 16;  // from one Q tile to the other
             for (int a = 0; a < accs && ok; ++a)
               ok = wait(bar_acc_empty + 8 * ((acc + a) & 1), ((uint32_t)((acc + a) >> 1) & 1u) ^ 1u,
                         kWaitLimitNs);
             if (!ok) break;
             tc_fence_after();
-            const int b0 = kF32 ? s * kSumBlocks : 0;
-            const int b1 = kF32 ? min(U.blocks, b0 + kSumBlocks) : U.blocks;
-            for (int b = b0; b < b1 && ok; ++b) {
+            for (int b = 0; b < U.blocks; ++b) {
               if (b == U.blocks - 1) next = take(seq + 1, N);
               ok = wait(bar_full + 8 * ring.bar, ring.phase, kWaitLimitNs);
               if (!ok) break;
               tc_fence_after();
               const uint32_t sp = s_ring + ring.place(bytes);
-              const uint64_t dp = operand_desc<kPMn>(sp);
-              uint64_t dq = operand_desc<kQMn>(sp + kPBytes);
+              const uint64_t dp = operand_desc<kPMn>(sp), dq = operand_desc<kQMn>(sp + kPBytes);
               const int steps = b == U.blocks - 1 ? (U.rem + 15) >> 4 : BT / 16;
-              for (int a = 0; a < accs; ++a) {
-                const uint32_t d = tmem + 256 * ((acc + a) & 1), idesc = a ? idesc_b : idesc_a;
-                mma_pair_f16(d, dp, dq, idesc, b != b0);
-                if (steps == BT / 16) {
-#pragma unroll
-                  for (int j = 1; j < BT / 16; ++j)
-                    mma_pair_f16(d, dp + j * kStep<kPMn>, dq + j * kStep<kQMn>, idesc, 1);
-                } else {
-                  for (int j = 1; j < steps; ++j)
-                    mma_pair_f16(d, dp + j * kStep<kPMn>, dq + j * kStep<kQMn>, idesc, 1);
-                }
-                dq += to_b;
-              }
+              multiply(tmem + 256 * (acc & 1), dp, dq, idesc_a, steps, b != 0);
+              if (accs == 2) multiply(tmem + 256 * ((acc + 1) & 1), dp, dq + to_b, idesc_b, steps, b != 0);
               tc_commit_pair_mc(bar_empty + 8 * ring.bar, kBoth);
               ring.next_block();
             }
             if (!ok) break;
-            for (int a = 0; a < accs; ++a) tc_commit_pair_mc(bar_acc_full + 8 * ((acc + a) & 1), kBoth);
+            for (int a = 0; a < accs; ++a, ++acc) tc_commit_pair_mc(bar_acc_full + 8 * (acc & 1), kBoth);
           }
         }
         // so do the odd CTA's last releases
@@ -675,39 +779,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (kMode == kGrad && warp == 3) {
       // -------------------------------------- rows past the segment's last
       const uint32_t lead_full = mapa_shared(bar_full, 0);
-      Ring<kRing> ring;
+      int ps = 0, qs = 0;   // slots of the unit's first blocks
       uint32_t parity = 0;  // of each tail barrier
-      for (int seq = 0;; ++seq) {
+      bool ok = true;
+      for (int seq = 0; ok; ++seq) {
         Unit U;
         if (!take_warp(seq, U)) break;
         __syncwarp();
         if (lane == 0) release_unit(seq);
         if (U.end) break;
-        const uint32_t bytes = block_bytes(U.n[0], U.n[1]);
-        uint32_t at = 0;
-        int bar = 0;
-        for (int b = 0; b < U.blocks; ++b) {
-          at = ring.place(bytes);
-          bar = ring.bar;
-          ring.next_block();
-        }
-        if (U.blocks == 0 || (U.rem & 15) == 0) continue;
-        if (!wait_warp(bar_tail + 8 * bar, (parity >> bar) & 1u, unit_limit)) break;
-        // a row: 8 pieces of 16 bytes in each column block of each tile
-        const int first = U.rem + (lane >> 3), last = (U.rem + 15) & ~15;
-        for (uint32_t block = at; block < at + bytes; block += 8192) {
-          uint8_t *base = smem + block + (lane & 7) * 16;
+        if (U.blocks == 0) continue;
+        // a row: 8 pieces of 16 bytes in each column block
+        auto zero = [&](int slot, uint32_t bytes) {
+          const int first = U.rem + (lane >> 3), last = (U.rem + 15) & ~15;
+          for (uint32_t block = 0; block < bytes; block += 8192) {
+            uint8_t *base = smem + slot * kPBytes + block + (lane & 7) * 16;
 #pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            if (first + i < last) *reinterpret_cast<uint4 *>(base + (first + i) * 128) = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < 16; i += 4)
+              if (first + i < last) *reinterpret_cast<uint4 *>(base + (first + i) * 128) = make_uint4(0, 0, 0, 0);
+          }
+        };
+        if (U.rem & 15) {
+          const int b0 = (U.blocks - 1) / U.chunk * U.chunk, n = U.blocks - b0;  // the last chunk
+          for (int g = 0; g < U.tiles; ++g) {
+            const int q = (qs + U.tiles * b0 + (g + 1) * n - 1) % kQSlots;
+            ok = wait_warp(bar_tail + 8 * q, (parity >> q) & 1u, unit_limit);
+            if (!ok) break;
+            parity ^= 1u << q;
+            if (g == 0) zero((ps + U.blocks - 1) % kPSlots, kPBytes);
+            zero(kPSlots + q, grad_n(U.nq, g) / 2 * (BT * 2));
+            // The fence has the zeros in this SM's shared memory, where the pair's MMAs read
+            // them.  (An arrival with cluster-wide release would also wait for whatever the SM
+            // is storing: 2000 to 3700 cycles a unit.)
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(lead_full + 8 * q);
+          }
         }
-        fence_async_shared();
-        __syncwarp();
-        // The fence has the zeros in this SM's shared memory, where the pair's MMAs read them.
-        // (An arrival with cluster-wide release would also wait for whatever the SM is storing:
-        // 2000 to 3700 cycles a unit.)
-        if (lane == 0) mbar_arrive_remote(lead_full + 8 * bar);
-        parity ^= 1u << bar;
+        ps = (ps + U.blocks) % kPSlots;
+        qs = (qs + U.tiles * U.blocks) % kQSlots;
       }
     }
   } else {
@@ -735,63 +845,100 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_remote(lead_acc_empty + 8 * buf);
       };
       if constexpr (kF32) {
-        float sum[4][32];
+        const int sums = (U.blocks + kSumBlocks - 1) / kSumBlocks;
+        for (int g = 0; ok && g < U.tiles; ++g) {
+          const int q0 = U.q0 + BQ * g, nq = U.nq - BQ * g;
+          float sum[4][32];
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 32; ++j) sum[g][j] = 0.0f;
-        const int sums = sums_of(U);
-        for (int s = 0; s < sums; ++s, ++acc) {
-          const int buf = acc & 1;
-          if (!wait_warp(bar_acc_full + 8 * buf, (uint32_t)(acc >> 1) & 1u, unit_limit)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (U.blocks > 0) {  // a segment without rows: nothing was accumulated
+            for (int j = 0; j < 32; ++j) sum[i][j] = 0.0f;
+          for (int s = 0; s < sums; ++s, ++acc) {
+            const int buf = acc & 1;
+            if (!wait_warp(bar_acc_full + 8 * buf, (uint32_t)(acc >> 1) & 1u, unit_limit)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const int c = 32 * (half + 2 * g);
-              if (c < U.nq) {
+            for (int i = 0; i < 4; ++i) {
+              const int c = 32 * (half + 2 * i);
+              if (c < nq) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   uint32_t v[16];
                   tmem_ld_x16(t_lane + 256 * buf + c + 16 * h, v);
                   tc_wait_ld();
 #pragma unroll
-                  for (int j = 0; j < 16; ++j) sum[g][16 * h + j] += __uint_as_float(v[j]);
+                  for (int j = 0; j < 16; ++j) sum[i][16 * h + j] += __uint_as_float(v[j]);
                 }
               }
             }
+            release(buf);
           }
-          release(buf);
-        }
-        if (!ok) break;
-        // 16 q's x 32 p at a time through the warp's two staging blocks; with accumulate the
-        // copy adds to the output in L2 (each value once, so in no particular order).  A block
-        // is written only if its copy follows: the wait counts copies.
-        if (pw >= P.np) continue;
+          // 16 q's x 32 p at a time through the warp's two staging blocks; with accumulate the
+          // copy adds to the output in L2 (each value once, so in no particular order; sums
+          // that start from loads of the output, 823 us against 770 for 16 x 4096 x 7168).
+          // A block is written only if its copy follows: the wait counts copies.
+          if (!ok || pw >= P.np) continue;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int c = 32 * (half + 2 * g);
+          for (int i = 0; i < 4; ++i) {
+            const int c = 32 * (half + 2 * i);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (c + 16 * h < U.nq) {
-              if (elect_one()) bulk_wait_read<1>();
-              __syncwarp();
-              float *row = reinterpret_cast<float *>(stage0_ptr + turn) + lane;
+            for (int h = 0; h < 2; ++h) {
+              if (c + 16 * h < nq) {
+                if (elect_one()) bulk_wait_read<1>();
+                __syncwarp();
+                float *row = reinterpret_cast<float *>(stage0_ptr + turn) + lane;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) row[32 * j] = sum[g][16 * h + j];
-              fence_async_shared();
-              __syncwarp();
-              if (elect_one()) {
-                if (P.accumulate)
-                  tma_add(&M.out, stage0 + turn, pw, U.q0 + c + 16 * h, U.z);
-                else
-                  tma_store(&M.out, stage0 + turn, pw, U.q0 + c + 16 * h, U.z);
-                bulk_commit();
+                for (int j = 0; j < 16; ++j) row[32 * j] = sum[i][16 * h + j];
+                fence_async_shared();
+                __syncwarp();
+                if (elect_one()) {
+                  if (P.accumulate)
+                    tma_add(&M.out, stage0 + turn, pw, q0 + c + 16 * h, U.z);
+                  else
+                    tma_store(&M.out, stage0 + turn, pw, q0 + c + 16 * h, U.z);
+                  bulk_commit();
+                }
+                turn ^= kStage;  // the other block next, whichever q's are left out
               }
-              turn ^= kStage;  // the other block next, whichever q's are left out
+            }
+          }
+        }
+      } else if constexpr (kMode == kGrad) {
+        for (int g = 0; g < U.tiles; ++g) {
+          const int buf = acc & 1, q0 = U.q0 + BQ * g, nq = min(BQ, U.nq - BQ * g);
+          const bool some = U.blocks > 0;  // else nothing was accumulated
+          if (some) {
+            if (!wait_warp(bar_acc_full + 8 * buf, (uint32_t)(acc >> 1) & 1u, unit_limit)) {
+              ok = false;
+              break;
+            }
+            ++acc;
+            tc_fence_after();
+          }
+          uint32_t v[32], w[16];
+          if (32 * half < nq)
+            load_columns(t_lane + 256 * buf + 32 * half, v);
+          else if (some)
+            release(buf);
+#pragma unroll 1
+          for (int c = 32 * half; c < nq; c += 64) {
+            tc_wait_ld();
+            round_columns<O>(v, !some, w);
+            if (c + 64 < nq)
+              load_columns(t_lane + 256 * buf + c + 64, v);  // on their way during the stores
+            else if (some)
+              release(buf);
+            if (elect_one()) bulk_wait_read<0>();  // the block's last copy has left it
+            __syncwarp();
+            stage_rows(w, stage0, lane);
+            fence_async_shared();
+            __syncwarp();
+            if (pw < P.np && elect_one()) {  // what passes the extents is left out
+              tma_store(&M.out, stage0, pw, q0 + c, U.z);
+              bulk_commit();
             }
           }
         }
@@ -805,37 +952,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const int q0 = a ? U.n[0] : 0, nq = a ? U.nq - U.n[0] : min(U.nq, U.n[0]);
-          if constexpr (kMode == kGrad) {
-            uint32_t v[32], w[16];
-            if (32 * half < nq) load_columns(t_lane + 256 * buf + 32 * half, v);
+          uint16_t *out = static_cast<uint16_t *>(P.out) + pw + (int64_t)(U.q0 + q0) * P.np;
 #pragma unroll 1
-            for (int c = 32 * half; c < nq; c += 64) {
-              tc_wait_ld();
-              round_columns<O>(v, U.blocks == 0, w);  // no blocks: nothing was accumulated
-              if (c + 64 < nq)
-                load_columns(t_lane + 256 * buf + c + 64, v);  // on their way during the stores
-              else
-                release(buf);
-              if (elect_one()) bulk_wait_read<0>();  // the block's last copy has left it
-              __syncwarp();
-              stage_rows(w, stage0, lane);
-              fence_async_shared();
-              __syncwarp();
-              if (pw < P.np && elect_one()) {  // what passes the extents is left out
-                tma_store(&M.out, stage0, pw, U.q0 + q0 + c, U.z);
-                bulk_commit();
-              }
-            }
-          } else {
-            uint16_t *out = static_cast<uint16_t *>(P.out) + pw + (int64_t)(U.q0 + q0) * P.np;
-#pragma unroll 1
-            for (int c = 32 * half; c < nq; c += 64) {
-              uint32_t v[32];
-              MOE_TMEM_LD_32x32b_X32(t_lane + 256 * buf + c, v);
-              tc_wait_ld();
-              if (c + 64 >= nq) release(buf);
-              store_columns<O>(v, out + (int64_t)c * P.np, P.np, nq - c, pw + lane < P.np, lane);
-            }
+          for (int c = 32 * half; c < nq; c += 64) {
+            uint32_t v[32];
+            MOE_TMEM_LD_32x32b_X32(t_lane + 256 * buf + c, v);
+            tc_wait_ld();
+            if (c + 64 >= nq) release(buf);
+            store_columns<O>(v, out + (int64_t)c * P.np, P.np, nq - c, pw + lane < P.np, lane);
           }
           if (32 * half >= nq) release(buf);
         }
@@ -1005,6 +1129,10 @@ extern "C" int moe_grouped_wgrad(const moe_wgrad_args *a, void *stream) {
   P.accumulate = a->accumulate != 0;
   P.p_blocked = a->k % BT == 0;
   P.q_blocked = a->n % BT == 0;
+  // More Q tiles a unit read P less often; eight units a pair and more keep the pairs even.
+  const int64_t tiles = (int64_t)a->seg.E * ((a->k + BP - 1) / BP) * ((a->n + BQ - 1) / BQ);
+  const int64_t pairs = std::max(1, (a->num_sms > 0 ? a->num_sms : device_sm_count()) / 2);
+  P.group = (int)std::min<int64_t>(8, std::max<int64_t>(1, tiles / (8 * pairs)));
   // without rows every segment is empty: the maps are not used, and need only be valid
   const bool f32 = a->out_type == MOE_TYPE_F32, none = a->seg.rows == 0;
   const uint64_t E = a->seg.E, n = a->n, k = a->k, rows = none ? 1 : a->seg.rows;
@@ -1013,8 +1141,7 @@ extern "C" int moe_grouped_wgrad(const moe_wgrad_args *a, void *stream) {
   for (int i = 0; i < 2; ++i) ok = ok && map_mn_major(&maps.q[i], none ? a->out : a->dy, 1, rows, n, i + 1);
   ok = ok && make_map(&maps.out, a->out, E, n, k, f32 ? 16 : 32, 32, f32);
   if (!ok) return MOE_ERR_CUDA;
-  const int64_t max_units =
-      (int64_t)a->seg.E * ((a->k + BP - 1) / BP) * ((a->n + BQ - 1) / BQ);
+  const int64_t max_units = tiles;
   if (max_units > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (f32)
     return launch<kGrad, float>(maps, P, max_units, a->num_sms, stream);
