@@ -16,6 +16,10 @@
 // work is one expert, 256 p and up to 256 q (one accumulator; the other takes the next
 // unit's MMAs while this one's is stored) or 512 (both: the P tile is read once for the two,
 // 48 KB a block for 1024 cycles).  Units that share weights run side by side on the 76 pairs.
+// The gradient's t is short, its output large: a unit there is 256 p and several Q tiles, one
+// after the other, and the P tiles of the whole segment stay in shared memory meanwhile (of a
+// longer one, chunk by chunk for two Q tiles).  Reading P once a Q tile instead bound it by
+// L2 reads (12 TB/s): 16 experts of ~512 rows 346 us, now 310; of 2048, 1026 and 969.
 //   warp 0  producer: TMA tiles into a ring in shared memory (128-byte swizzle).  An operand
 //           whose contiguous index is t (forward: both; trans: Q) is K-major, the others are
 //           MN-major in 64-wide column blocks: nothing is transposed by anyone.  The
@@ -42,11 +46,12 @@
 //     in each SM; 64 KB gave 4.6 TB/s.
 //   about 256 rows, ragged: weights, rows and output from and to HBM, 676 us (6.1 TB/s).
 //   many rows: the tensor cores under the power cap, 1560 to 1960 TFLOP/s.
-//   gradient, 16 experts of about 256 rows: 214 us, 4.4 TB/s of writes; zeros alone are
-//     written at 6.9 TB/s, the MMAs alone would take 110 us.
+//   gradient, 16 experts of about 256 rows: 195 us, 4.8 TB/s of writes, shared memory 78 %
+//     busy (copies in, MMAs, staging); zeros alone are written at 6.9 TB/s, the MMAs alone
+//     would take 110 us.  2048 rows: 969 us, 1985 TFLOP/s.
 // Tried and not kept: requests into L2 ahead of the ring (560 -> 667 us, they queue before
 // the ring's own copies), Q multicast over clusters of two pairs (152 SMs hold 36 of them:
-// 5 % slower), 128-deep blocks for the gradient.
+// 5 % slower), 128-deep blocks for the gradient, fewer slots for its Q (5: 197 us, 4: 213).
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -64,18 +69,19 @@ constexpr int kWide = 2 * BQ;               // q's of a unit with both accumulat
 constexpr int kUnitQ = 8;
 constexpr uint32_t kPBytes = 128 * BT * 2;  // a CTA's half of a P tile
 // Bytes of the operand ring, and of an epilogue warp's staging (gradient): a block of 32 x
-// 32 16-bit values, or two in turn of 16 x 32 binary32 ones.
+// 32 16-bit values, or three in turn of 16 x 32 binary32 ones.
 constexpr uint32_t kStage = 2048;
-constexpr uint32_t ring_bytes(int mode, bool f32) { return (mode != kGrad ? 212 : f32 ? 180 : 196) * 1024; }
-constexpr uint32_t stage_bytes(int mode, bool f32) { return mode != kGrad ? 0 : f32 ? 2 * kStage : kStage; }
+constexpr int kStages = 3;  // (two and six P slots: 464 against 434 us, 16 x ~512 rows)
+constexpr uint32_t ring_bytes(int mode, bool f32) { return (mode != kGrad ? 212 : f32 ? 164 : 196) * 1024; }
+constexpr uint32_t stage_bytes(int mode, bool f32) { return mode != kGrad ? 0 : f32 ? kStages * kStage : kStage; }
 constexpr int kSumBlocks = 8;  // blocks of one partial sum (binary32 output): 512 rows
 // Slots of the gradient's operands, 16 KB each: P tiles stay while several Q tiles pass.  A Q
 // slot's barriers serve a P tile too where one comes along.  Every use of a P tile has a Q tile
 // of its own, so by the time that the Q slot of a block is free again, so is a P slot loaded
 // as many P tiles ago as there are Q slots, or more.
-constexpr int kPSlots = 6;
-constexpr int q_slots(bool f32) { return (int)(ring_bytes(2, f32) / (16 * 1024)) - kPSlots; }
-static_assert(q_slots(false) <= kPSlots && q_slots(true) <= kPSlots, "P slots are reused by Q's barriers");
+constexpr int p_slots(bool f32) { return f32 ? 5 : 6; }
+constexpr int q_slots(bool f32) { return (int)(ring_bytes(2, f32) / (16 * 1024)) - p_slots(f32); }
+static_assert(q_slots(false) <= p_slots(false) && q_slots(true) <= p_slots(true), "P slots are reused by Q's barriers");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -321,21 +327,22 @@ __device__ __forceinline__ void split_n(Unit &U) {
 // MMAs of the other.  Long sums in registers leave room for one Q tile.
 template <bool kF32>
 __device__ __forceinline__ int grad_tiles(int group, int count) {
-  return count <= kPSlots * BT ? group : kF32 ? 1 : min(group, 2);
+  return count <= p_slots(kF32) * BT ? group : kF32 ? 1 : min(group, 2);
 }
 template <bool kF32>
 __device__ __forceinline__ int grad_chunk(int blocks) {
-  if (blocks <= kPSlots) return max(blocks, 1);
+  if (blocks <= p_slots(kF32)) return max(blocks, 1);
   if (kF32) return kSumBlocks;
-  const int chunks = (blocks + kPSlots - 1) / kPSlots;
+  const int chunks = (blocks + p_slots(kF32) - 1) / p_slots(kF32);
   return (blocks + chunks - 1) / chunks;
 }
 // N of the MMAs of Q tile g: whole 64-wide column blocks in each CTA.
 __device__ __forceinline__ int grad_n(int nq, int g) { return nq - BQ * g > BQ / 2 ? BQ : BQ / 2; }
 
-// Unit u: the segments in order, within one the p tiles, within one the row tiles (or, for
-// the gradient, the q tiles), so units that share a weight tile run side by side.  e: the
-// segment of the caller's last unit, or -1.
+// Unit u: the segments in order, within one the p tiles, within one the row tiles, so units
+// that share a weight tile run side by side; for the gradient the groups of q tiles, within
+// one the p tiles, so whole rows of the output are stored at a time (binary32, ~512 rows: 460
+// us the other way, 434 this).  e: the segment of the caller's last unit, or -1.
 template <int kMode, bool kF32>
 __device__ __forceinline__ Unit get_unit(const GroupedParams &P, const SegTable &T, int u,
                                          int p_tiles, int &e) {
@@ -343,7 +350,14 @@ __device__ __forceinline__ Unit get_unit(const GroupedParams &P, const SegTable 
   if (e < 0 || u >= T.before[e + 1] * p_tiles) e = find_segment(T, P.seg.E, u, p_tiles);
   const int tiles = T.before[e + 1] - T.before[e];  // q tiles of the segment
   const int local = u - T.before[e] * p_tiles, count = T.count[e];
-  const int pt = tiles == 1 ? local : local / tiles, qt = local - pt * tiles;
+  int pt, qt;
+  if constexpr (kMode == kGrad) {
+    qt = local / p_tiles;
+    pt = local - qt * p_tiles;
+  } else {
+    pt = tiles == 1 ? local : local / tiles;
+    qt = local - pt * tiles;
+  }
   U.z = e;
   U.p0 = pt * BP;
   if constexpr (kMode == kGrad) {
@@ -434,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kF32 = sizeof(O) == 4;
   constexpr uint32_t kRing = ring_bytes(kMode, kF32);
   constexpr bool kPMn = kMode != kFwd, kQMn = kMode == kGrad;
-  constexpr int kQSlots = q_slots(kF32);
+  constexpr int kPSlots = p_slots(kF32), kQSlots = q_slots(kF32);
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -829,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lead_acc_empty = mapa_shared(bar_acc_empty, 0);
     uint8_t *stage0_ptr = smem + kRing + (warp - 4) * stage_bytes(kMode, kF32);
     const uint32_t stage0 = smem_u32(stage0_ptr);
-    uint32_t turn = 0;
+    int turn = 0;
     int acc = 0;
     bool ok = true;
     for (int seq = 0; ok; ++seq) {
@@ -847,7 +861,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (kF32) {
         const int sums = (U.blocks + kSumBlocks - 1) / kSumBlocks;
         for (int g = 0; ok && g < U.tiles; ++g) {
-          const int q0 = U.q0 + BQ * g, nq = U.nq - BQ * g;
+          const int q0 = U.q0 + BQ * g, nq = min(BQ, U.nq - BQ * g);
+          // Piece i of the warp's eight: 16 q's x 32 p, through its staging blocks in turn.
+          auto piece_q = [&](int i) { return 32 * (half + 2 * (i >> 1)) + 16 * (i & 1); };
+          auto block = [&](int i) { return (turn + i) % kStages; };
           float sum[4][32];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -876,35 +893,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             release(buf);
           }
-          // 16 q's x 32 p at a time through the warp's two staging blocks; with accumulate the
-          // copy adds to the output in L2 (each value once, so in no particular order; sums
-          // that start from loads of the output, 823 us against 770 for 16 x 4096 x 7168).
-          // A block is written only if its copy follows: the wait counts copies.
+          // With accumulate the copy adds to the output in L2 (each value once, so in no
+          // particular order): 4.95 TB/s read and written.  Loads of the output beside the
+          // MMAs and stores of the sums: 774 us against 760 (16 x ~256 rows); by each lane for
+          // itself, 823; stores by lane instead of copies, 620 us against 362 (binary32,
+          // nothing added).  A block is written only if its copy follows: the wait counts copies.
           if (!ok || pw >= P.np) continue;
+          int done = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = 32 * (half + 2 * i);
+          for (int i = 0; i < 8; ++i) {
+            if (piece_q(i) < nq) {
+              const int k = block(i);
+              done = i + 1;
+              float *row = reinterpret_cast<float *>(stage0_ptr + k * kStage) + lane;
+              if (elect_one()) bulk_wait_read<kStages - 1>();
+              __syncwarp();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (c + 16 * h < nq) {
-                if (elect_one()) bulk_wait_read<1>();
-                __syncwarp();
-                float *row = reinterpret_cast<float *>(stage0_ptr + turn) + lane;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) row[32 * j] = sum[i][16 * h + j];
-                fence_async_shared();
-                __syncwarp();
-                if (elect_one()) {
-                  if (P.accumulate)
-                    tma_add(&M.out, stage0 + turn, pw, q0 + c + 16 * h, U.z);
-                  else
-                    tma_store(&M.out, stage0 + turn, pw, q0 + c + 16 * h, U.z);
-                  bulk_commit();
-                }
-                turn ^= kStage;  // the other block next, whichever q's are left out
+              for (int j = 0; j < 16; ++j) row[32 * j] = sum[i >> 1][16 * (i & 1) + j];
+              fence_async_shared();
+              __syncwarp();
+              if (elect_one()) {
+                if (P.accumulate)
+                  tma_add(&M.out, stage0 + k * kStage, pw, q0 + piece_q(i), U.z);
+                else
+                  tma_store(&M.out, stage0 + k * kStage, pw, q0 + piece_q(i), U.z);
+                bulk_commit();
               }
             }
           }
+          turn = block(done);
         }
       } else if constexpr (kMode == kGrad) {
         for (int g = 0; g < U.tiles; ++g) {
