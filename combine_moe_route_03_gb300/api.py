@@ -689,7 +689,8 @@ class MoELayer:
         self.A_sf = t(scale_bytes(rows, H, afmt))
         self.H1 = t(rows, I)
         self.H1_sf = t(scale_bytes(rows, I, afmt))
-        self.Y = t(rows, H, dtype=torch.bfloat16)
+        # rows without a token are never written: they hold zeros, not what was in memory
+        self.Y = t(rows, H, dtype=torch.bfloat16).zero_()
         self.S = self.Y[self.rows:] if cfg.shared else None
         self.signal = t(rows // cfg.block_m_signal, dtype=torch.int32) if cfg.sbo else None
         self.src_of = t(self.rows, dtype=torch.int32) if cfg.fuse_combine else None
