@@ -19,7 +19,7 @@
 // The gradient's t is short, its output large: a unit there is 256 p and several Q tiles, one
 // after the other, and the P tiles of the whole segment stay in shared memory meanwhile (of a
 // longer one, chunk by chunk for two Q tiles).  Reading P once a Q tile instead bound it by
-// L2 reads (12 TB/s): 16 experts of ~512 rows 346 us, now 310; of 2048, 1026 and 969.
+// L2 reads (12 TB/s): 16 experts of ~512 rows 346 us, now 307; of 2048, 1026 and 961.
 //   warp 0  producer: TMA tiles into a ring in shared memory (128-byte swizzle).  An operand
 //           whose contiguous index is t (forward: both; trans: Q) is K-major, the others are
 //           MN-major in 64-wide column blocks: nothing is transposed by anyone.  The
@@ -46,9 +46,9 @@
 //     in each SM; 64 KB gave 4.6 TB/s.
 //   about 256 rows, ragged: weights, rows and output from and to HBM, 676 us (6.1 TB/s).
 //   many rows: the tensor cores under the power cap, 1560 to 1960 TFLOP/s.
-//   gradient, 16 experts of about 256 rows: 195 us, 4.8 TB/s of writes, shared memory 78 %
+//   gradient, 16 experts of about 256 rows: 191 us, 4.9 TB/s of writes, shared memory 78 %
 //     busy (copies in, MMAs, staging); zeros alone are written at 6.9 TB/s, the MMAs alone
-//     would take 110 us.  2048 rows: 969 us, 1985 TFLOP/s.
+//     would take 110 us.  2048 rows: 961 us, 2000 TFLOP/s.
 // Tried and not kept: requests into L2 ahead of the ring (560 -> 667 us, they queue before
 // the ring's own copies), Q multicast over clusters of two pairs (152 SMs hold 36 of them:
 // 5 % slower), 128-deep blocks for the gradient, fewer slots for its Q (5: 197 us, 4: 213).
@@ -321,20 +321,21 @@ __device__ __forceinline__ void split_n(Unit &U) {
   }
 }
 // The gradient's Q tiles of a unit.  A short segment's P tiles all stay in their slots: one
-// Q tile after the other passes over them (chunk: every block), with as many Q tiles as the
-// host allows.  A long segment's pass in chunks, each Q tile in its own accumulator, so two.
-// Either way each P tile is read once for all of them, and an accumulator is stored beside the
-// MMAs of the other.  Long sums in registers leave room for one Q tile.
+// Q tile after the other passes over them (chunk: every block), as many as the host allows.  A
+// long segment's pass in chunks, each Q tile in its own accumulator, so two.  Either way each P
+// tile is read once for all of them, and an accumulator is stored beside the MMAs of the other.
+// Binary32 outputs, where twice the stores bound a tile, take one (16 experts, 4096 x 7168,
+// ~256 rows: 332 us against 352 in eights; 32 experts, 2048 x 2048, ~128 rows: 102 and 112),
+// and long sums in registers leave no room for more.
 template <bool kF32>
 __device__ __forceinline__ int grad_tiles(int group, int count) {
-  return count <= p_slots(kF32) * BT ? group : kF32 ? 1 : min(group, 2);
+  return kF32 ? 1 : count <= p_slots(false) * BT ? group : min(group, 2);
 }
 template <bool kF32>
 __device__ __forceinline__ int grad_chunk(int blocks) {
-  if (blocks <= p_slots(kF32)) return max(blocks, 1);
   if (kF32) return kSumBlocks;
-  const int chunks = (blocks + p_slots(kF32) - 1) / p_slots(kF32);
-  return (blocks + chunks - 1) / chunks;
+  const int chunks = (blocks + p_slots(false) - 1) / p_slots(false);
+  return (blocks + chunks - 1) / max(chunks, 1);
 }
 // N of the MMAs of Q tile g: whole 64-wide column blocks in each CTA.
 __device__ __forceinline__ int grad_n(int nq, int g) { return nq - BQ * g > BQ / 2 ? BQ : BQ / 2; }
@@ -1146,10 +1147,12 @@ extern "C" int moe_grouped_wgrad(const moe_wgrad_args *a, void *stream) {
   P.accumulate = a->accumulate != 0;
   P.p_blocked = a->k % BT == 0;
   P.q_blocked = a->n % BT == 0;
-  // More Q tiles a unit read P less often; eight units a pair and more keep the pairs even.
+  // More Q tiles a unit read P less often, fewer keep the pairs even: four where each pair
+  // still has 16 units and more (16 experts, 4096 x 7168, ~256 rows: 206 us in ones, 196 in
+  // twos, 194 in fours, 203 in sixteens; 32 experts, 2048 x 2048: 57.9 in ones, 60.0 in threes).
   const int64_t tiles = (int64_t)a->seg.E * ((a->k + BP - 1) / BP) * ((a->n + BQ - 1) / BQ);
   const int64_t pairs = std::max(1, (a->num_sms > 0 ? a->num_sms : device_sm_count()) / 2);
-  P.group = (int)std::min<int64_t>(8, std::max<int64_t>(1, tiles / (8 * pairs)));
+  P.group = (int)std::min<int64_t>(4, std::max<int64_t>(1, tiles / (16 * pairs)));
   // without rows every segment is empty: the maps are not used, and need only be valid
   const bool f32 = a->out_type == MOE_TYPE_F32, none = a->seg.rows == 0;
   const uint64_t E = a->seg.E, n = a->n, k = a->k, rows = none ? 1 : a->seg.rows;

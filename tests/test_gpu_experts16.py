@@ -655,7 +655,8 @@ def test_operators_in_a_captured_graph(dev):
     assert torch.equal(out, want) and torch.equal(h, api.swiglu(want, counts=counts))
 
 
-@pytest.mark.parametrize("counts", [[45, 274, 115, 60, 50, 35], [9, 0, 900, 1300]])
+@pytest.mark.parametrize("counts", [[45, 274, 115, 60, 50, 35], [9, 0, 900, 1300],
+                                    [319, 320, 321, 384, 385, 448, 449, 513, 0, 769]])
 @pytest.mark.parametrize("n,k", [(5792, 1984), (1232, 672), (4288, 376)])
 def test_many_units_a_pair_with_partial_tiles_between(dev, counts, n, k):
     """Each CTA pair works through several tiles, whole ones and ones that pass the extents
