@@ -685,3 +685,24 @@ def test_many_units_a_pair_with_partial_tiles_between(dev, counts, n, k):
         assert torch.equal(api.grouped_wgrad(dy, x, c, out_dtype=F32), dw)
         api.grouped_wgrad(dy, x, c, out=acc, accumulate=True)
         assert torch.equal(acc, base + (turn + 1) * dw)
+
+
+@pytest.mark.parametrize("align", [1, 64])
+@pytest.mark.parametrize("n,k", [(1232, 672), (4288, 2056)])
+def test_wgrad_keeps_what_follows_a_segment_out(dev, n, k, align):
+    """Every number of rows past a segment's last multiple of 16, with the next segment's rows
+    (align 1) or NaN (align 64) behind it, tile after tile on every pair.  Whole numbers:
+    equality."""
+    gen = torch.Generator("cuda").manual_seed(21)
+    counts = [i + 16 * (i % 5) for i in range(1, 16)] + [64, 79, 127, 0, 400, 513]
+    rows, starts, c = rows_of(counts, align), starts_of(counts, align), i32(counts)
+    dy = torch.full((rows, n), float("nan"), dtype=BF16, device=dev)
+    x = torch.full((rows, k), float("nan"), dtype=BF16, device=dev)
+    want = torch.zeros(len(counts), n, k, device=dev)
+    for e, (m, s) in enumerate(zip(counts, starts)):
+        dy[s:s + m] = torch.randint(-3, 4, (m, n), generator=gen, device=dev).to(BF16)
+        x[s:s + m] = torch.randint(-3, 4, (m, k), generator=gen, device=dev).to(BF16)
+        want[e] = (dy[s:s + m].double().t() @ x[s:s + m].double()).float()
+    for _ in range(10):
+        assert torch.equal(api.grouped_wgrad(dy, x, c, align=align), want.to(BF16))
+        assert torch.equal(api.grouped_wgrad(dy, x, c, align=align, out_dtype=F32), want)
