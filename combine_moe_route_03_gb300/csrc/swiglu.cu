@@ -85,12 +85,13 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluParams P) 
   const T *gu = static_cast<const T *>(P.gu), *dhp = static_cast<const T *>(P.dh);
   T *outp = static_cast<T *>(P.out);
   const int I = P.I;
-  // with kRow == kThreads the block meets at barriers: `v` is the same in all threads
-  for (int v = blockIdx.x * kGroups + group; v < total; v += gridDim.x * kGroups) {
-    int r = v;
+  // with kRow == kThreads the block meets at barriers: `v` is the same in all threads.  64
+  // bits: rows may number nearly 2^31, and the last step passes them by up to a grid's.
+  for (int64_t v = (int64_t)blockIdx.x * kGroups + group; v < total; v += (int64_t)gridDim.x * kGroups) {
+    int r = (int)v;
     if (P.seg.counts) {
-      const int e = find_segment(table, P.seg.E, v);
-      r = table.start[e] + (v - table.before[e]);
+      const int e = find_segment(table, P.seg.E, (int)v);
+      r = table.start[e] + ((int)v - table.before[e]);
     }
     const float w = P.row_w ? P.row_w[r] : 1.0f;
     const T *g_row = gu + (size_t)r * 2 * I, *dh_row = dhp + (size_t)r * I;

@@ -265,6 +265,29 @@ def test_offsets_past_31_bits(dev):
     assert not bool(h[:-5].any())
 
 
+def test_swiglu_of_the_largest_number_of_rows(dev):
+    """The last rows of the range: the step past them does not fit 31 bits."""
+    rows, ends = 2 ** 31 - 1 - 1024, 40_000
+    gen = torch.Generator("cuda").manual_seed(22)
+    gu = torch.zeros(rows, 2, dtype=BF16, device=dev)
+    dh = torch.zeros(rows, 1, dtype=BF16, device=dev)
+    for part in (slice(0, ends), slice(rows - ends, rows)):
+        gu[part], dh[part] = normal(gen, ends, 2), normal(gen, ends, 1)
+    for counts in (None, i32([5, rows - 70_000, 0, 69_995])):
+        h = api.swiglu(gu, counts=counts)
+        for part in (slice(0, ends), slice(rows - ends, rows)):
+            ref, slack = swiglu_reference(gu[part], None, None)
+            check_close(h[part], ref, slack, BF16)
+        assert not bool(h[ends:rows - ends].any())
+        del h
+        dgu, _ = api.swiglu_backward(gu, dh, counts=counts)
+        for part in (slice(0, ends), slice(rows - ends, rows)):
+            ref, slack, _, _ = swiglu_reference(gu[part], dh[part], None)
+            check_close(dgu[part], ref, slack, BF16)
+        assert not bool(dgu[ends:rows - ends].any())
+        del dgu
+
+
 def test_largest_number_of_experts(dev):
     gen = torch.Generator("cuda").manual_seed(6)
     E, n, k = 1024, 16, 24
