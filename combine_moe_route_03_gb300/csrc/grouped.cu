@@ -332,10 +332,11 @@ constexpr uint64_t kStep = kMnMajor ? 2048 / 16 : 32 / 16;
 // ------------------------------------------------------------------- schedule
 // Rows of a segment's row tiles: one tile of up to 256 (one accumulator, the other one
 // takes the next unit's MMAs meanwhile), else the fewest of up to 512 (both), evened out.
+// (Unsigned: count and tiles may together pass 2^31.)
 __device__ __forceinline__ int tile_rows(int count) {
   if (count <= kWide) return (count + 31) / 32 * 32;
-  const int tiles = (count + kWide - 1) / kWide;
-  return ((count + tiles - 1) / tiles + 31) / 32 * 32;
+  const unsigned tiles = ((unsigned)count + kWide - 1) / kWide;
+  return (int)((((unsigned)count + tiles - 1) / tiles + 31) / 32 * 32);
 }
 __device__ __forceinline__ int row_tiles(int count) {
   if (count <= kWide) return count > 0;

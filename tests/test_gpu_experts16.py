@@ -265,6 +265,29 @@ def test_offsets_past_31_bits(dev):
     assert not bool(h[:-5].any())
 
 
+@pytest.mark.parametrize("trans", [False, True])
+def test_grouped_gemm_of_the_largest_number_of_rows(dev, trans):
+    """One segment with every row of the range, and one behind a few others: whole numbers,
+    equality."""
+    rows, ends, part = 2 ** 31 - 1 - 1024, 5000, 2 ** 27
+    gen = torch.Generator("cuda").manual_seed(23)
+    x, out = (torch.empty(rows, 8, dtype=BF16, device=dev) for _ in range(2))
+    x.fill_(1.0)
+    for s in (slice(0, ends), slice(rows - ends, rows)):
+        x[s] = torch.randint(-3, 4, (ends, 8), generator=gen, device=dev).to(BF16)
+    w = torch.randint(-3, 4, (3, 8, 8), generator=gen, device=dev).to(BF16)
+    for counts in ([rows], [7, 0, rows - 7]):
+        status = api.new_status()
+        api.grouped_gemm(x, w[:len(counts)], i32(counts), trans=trans, out=out.fill_(-99.0), status=status)
+        assert api.read_status(status) == 0
+        m = w[len(counts) - 1].float() if trans else w[len(counts) - 1].float().t()
+        assert torch.equal(out[7:ends], (x[7:ends].float() @ m).to(BF16))
+        assert torch.equal(out[rows - ends:], (x[rows - ends:].float() @ m).to(BF16))
+        want = m.sum(0).to(BF16)
+        for at in range(ends, rows - ends, part):
+            assert bool((out[at:min(at + part, rows - ends)] == want).all())
+
+
 def test_swiglu_of_the_largest_number_of_rows(dev):
     """The last rows of the range: the step past them does not fit 31 bits."""
     rows, ends = 2 ** 31 - 1 - 1024, 40_000
