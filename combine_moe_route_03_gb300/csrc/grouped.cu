@@ -35,9 +35,13 @@
 //           from registers, which leaves the ring 212 KB; the gradient, whose units are
 //           short and bound by their stores, hands blocks of 32 x 32 to bulk copies.
 // The tensor core's binary32 accumulation truncates: the relative error grows with the
-// number of additions (measured 1e-6 at t = 1024 and 1.9e-5 at 16384).  16-bit outputs
-// round far above that; binary32 gradients take partial sums of 512 rows and add them in
-// the epilogue's registers with rounding to nearest.
+// number of additions (measured 1e-6 at t = 1024 and 1.9e-5 at 16384).  So long sums are
+// joined: partial sums are added in the epilogue's registers with rounding to nearest.
+// Binary32 gradients take 512 rows a partial sum.  16-bit outputs round far above the error
+// of a sum of up to 16384 terms (fp16: 1/25 of its rounding) or 131072 (bf16, whose rounding
+// is 8 times as coarse); what is longer is joined from partial sums of 4096 (t = 20000, fp16,
+// 4096 x 2048 a product: forward 231 us against 210 in one sum, trans 223 and 210; gradient of
+// 160000 rows, 4096 x 2048: as fast as two Q tiles that share P).
 //
 // What bounds it, and what it measured (64 experts, n = 4096, k = 7168; 6.76 TB/s and 1864
 // TFLOP/s are a copy's and a dense library product's rates):
@@ -74,7 +78,9 @@ constexpr uint32_t kStage = 2048;
 constexpr int kStages = 3;  // (two and six P slots: 464 against 434 us, 16 x ~512 rows)
 constexpr uint32_t ring_bytes(int mode, bool f32) { return (mode != kGrad ? 212 : f32 ? 164 : 196) * 1024; }
 constexpr uint32_t stage_bytes(int mode, bool f32) { return mode != kGrad ? 0 : f32 ? kStages * kStage : kStage; }
-constexpr int kSumBlocks = 8;  // blocks of one partial sum (binary32 output): 512 rows
+constexpr int kSumBlocks = 8;    // blocks of one partial sum (binary32 output): 512 rows
+constexpr int kJoinBlocks = 64;  // of a joined sum with 16-bit output
+constexpr int kLongestF16 = 16384, kLongestBf16 = 131072;  // terms of a sum that is not joined
 // Slots of the gradient's operands, 16 KB each: P tiles stay while several Q tiles pass.  A Q
 // slot's barriers serve a P tile too where one comes along.  Every use of a P tile has a Q tile
 // of its own, so by the time that the Q slot of a block is free again, so is a P slot loaded
@@ -100,6 +106,7 @@ struct Unit {
   int blocks; // 64-deep blocks of t
   int rem;    // t's of the last block, 1..64
   int once;   // no other unit reads this P tile
+  int join;   // gradient: partial sums are joined by the epilogue (one Q tile a unit)
   int end;
 };
 
@@ -178,6 +185,7 @@ struct GroupedParams {
   int np, nq, nt;  // extents of p; of q (gradient: n); of t (forward, trans)
   int p_blocked, q_blocked;
   int group;  // gradient: most Q tiles of a unit
+  int longest; // most terms of a sum that is not joined (16-bit outputs)
   int bf16;
   int accumulate;
   void *out;
@@ -230,6 +238,13 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t *r) 
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// 16 columns, the same way.
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
       : "r"(taddr));
 }
 // Four 8x8 blocks of 16-bit values, each stored transposed; lane 8m + j gives the address
@@ -331,16 +346,17 @@ constexpr uint64_t kStep = kMnMajor ? 2048 / 16 : 32 / 16;
 
 // ------------------------------------------------------------------- schedule
 // Rows of a segment's row tiles: one tile of up to 256 (one accumulator, the other one
-// takes the next unit's MMAs meanwhile), else the fewest of up to 512 (both), evened out.
-// (Unsigned: count and tiles may together pass 2^31.)
-__device__ __forceinline__ int tile_rows(int count) {
-  if (count <= kWide) return (count + 31) / 32 * 32;
-  const unsigned tiles = ((unsigned)count + kWide - 1) / kWide;
+// takes the next unit's MMAs meanwhile), else the fewest of up to `wide` (512: both; 256 where
+// sums are joined, whose registers hold one), evened out.  (Unsigned: count and tiles may
+// together pass 2^31.)
+__device__ __forceinline__ int tile_rows(int count, int wide) {
+  if (count <= wide) return (count + 31) / 32 * 32;
+  const unsigned tiles = ((unsigned)count + wide - 1) / wide;
   return (int)((((unsigned)count + tiles - 1) / tiles + 31) / 32 * 32);
 }
-__device__ __forceinline__ int row_tiles(int count) {
-  if (count <= kWide) return count > 0;
-  const int rows = tile_rows(count);
+__device__ __forceinline__ int row_tiles(int count, int wide) {
+  if (count <= wide) return count > 0;
+  const int rows = tile_rows(count, wide);
   return (count + rows - 1) / rows;
 }
 // N of each accumulator for nq q's.
@@ -359,14 +375,17 @@ __device__ __forceinline__ void split_n(Unit &U) {
 // tile is read once for all of them, and an accumulator is stored beside the MMAs of the other.
 // Binary32 outputs, where twice the stores bound a tile, take one (16 experts, 4096 x 7168,
 // ~256 rows: 332 us against 352 in eights; 32 experts, 2048 x 2048, ~128 rows: 102 and 112),
-// and long sums in registers leave no room for more.
-template <bool kF32>
-__device__ __forceinline__ int grad_tiles(int group, int count) {
-  return kF32 ? 1 : count <= p_slots(false) * BT ? group : min(group, 2);
+// and joined sums in registers leave no room for more.
+template <bool kF32, bool kLong>
+__device__ __forceinline__ int grad_tiles(const GroupedParams &P, int count) {
+  if (kF32 || (kLong && count > P.longest)) return 1;
+  return count <= p_slots(false) * BT ? P.group : min(P.group, 2);
 }
+// Blocks of t that a Q tile takes at a time: of joined sums, those of one partial sum.
 template <bool kF32>
-__device__ __forceinline__ int grad_chunk(int blocks) {
+__device__ __forceinline__ int grad_chunk(int blocks, bool join) {
   if (kF32) return kSumBlocks;
+  if (join) return kJoinBlocks;
   const int chunks = (blocks + p_slots(false) - 1) / p_slots(false);
   return (blocks + chunks - 1) / max(chunks, 1);
 }
@@ -377,7 +396,7 @@ __device__ __forceinline__ int grad_n(int nq, int g) { return nq - BQ * g > BQ /
 // that share a weight tile run side by side; for the gradient the groups of q tiles, within
 // one the p tiles, so whole rows of the output are stored at a time (binary32, ~512 rows: 460
 // us the other way, 434 this).  e: the segment of the caller's last unit, or -1.
-template <int kMode, bool kF32>
+template <int kMode, bool kF32, bool kLong>
 __device__ __forceinline__ Unit get_unit(const GroupedParams &P, const SegTable &T, int u,
                                          int p_tiles, int &e) {
   Unit U = {};
@@ -395,16 +414,17 @@ __device__ __forceinline__ Unit get_unit(const GroupedParams &P, const SegTable 
   U.z = e;
   U.p0 = pt * BP;
   if constexpr (kMode == kGrad) {
-    const int q = grad_tiles<kF32>(P.group, count) * BQ;
+    const int q = grad_tiles<kF32, kLong>(P, count) * BQ;
     U.q0 = qt * q;
     U.nq = min(q, P.nq - U.q0);
     U.tiles = (U.nq + BQ - 1) / BQ;
     U.t0 = T.start[e];
     U.blocks = (count + BT - 1) / BT;
     U.rem = count - (U.blocks - 1) * BT;
-    U.chunk = grad_chunk<kF32>(U.blocks);
+    U.join = kF32 || (kLong && count > P.longest);
+    U.chunk = grad_chunk<kF32>(U.blocks, U.join);
   } else {
-    const int rows = tile_rows(count);
+    const int rows = tile_rows(count, kLong ? BQ : kWide);
     U.q0 = T.start[e] + qt * rows;
     U.nq = min(rows, count - qt * rows);
     split_n(U);
@@ -476,7 +496,9 @@ __device__ __forceinline__ void stage_rows(const uint32_t *w, uint32_t stage, in
     }
 }
 
-template <int kMode, class O>
+// kLong: 16-bit outputs with sums that may be longer than P.longest (forward and trans: that
+// are).  An instance of its own, so that the others keep their registers.
+template <int kMode, class O, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_kernel(const __grid_constant__ Maps M, const GroupedParams P) {
   constexpr bool kF32 = sizeof(O) == 4;
@@ -527,10 +549,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       P.seg, S.table, S.part,
       [&](int n) {
         if constexpr (kMode == kGrad) {
-          const int q = grad_tiles<kF32>(P.group, n) * BQ;
+          const int q = grad_tiles<kF32, kLong>(P, n) * BQ;
           return P.accumulate && n == 0 ? 0 : (P.nq + q - 1) / q;
         }
-        return row_tiles(n);
+        return row_tiles(n, kLong ? BQ : kWide);
       },
       cluster_id_x() == 0 && rank == 0);
   tc_fence_before();
@@ -729,12 +751,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             release_unit(seq);
             if (U.end) break;
             if (rank != 0) continue;  // the odd CTA only follows the unit stream
+            const bool join = kF32 || (kLong && U.join);
             for (int b0 = 0; ok && b0 < U.blocks; b0 += U.chunk) {
               const int b1 = min(U.blocks, b0 + U.chunk), first = ps;
               ps = (ps + b1 - b0) % kPSlots;
               for (int g = 0; ok && g < U.tiles; ++g) {
-                const int a = kF32 ? acc : acc + g;
-                const bool fresh = kF32 || b0 == 0;
+                const int a = join ? acc : acc + g;
+                const bool fresh = join || b0 == 0;
                 if (fresh) {
                   ok = wait(bar_acc_empty + 8 * (a & 1), ((uint32_t)(a >> 1) & 1u) ^ 1u, kWaitLimitNs);
                   if (!ok) break;
@@ -760,11 +783,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                   qs.next();
                   if (++at == kPSlots) at = 0;
                 }
-                if (ok && (kF32 || b1 == U.blocks)) tc_commit_pair_mc(bar_acc_full + 8 * (a & 1), kBoth);
-                if (kF32) ++acc;
+                if (ok && (join || b1 == U.blocks)) tc_commit_pair_mc(bar_acc_full + 8 * (a & 1), kBoth);
+                if (join) ++acc;
               }
             }
-            if (!kF32 && U.blocks > 0) acc += U.tiles;
+            if (!join && U.blocks > 0) acc += U.tiles;
           }
         } else {
           Ring<kRing> ring;
@@ -783,26 +806,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t idesc_a = idesc0 | ((uint32_t)(U.n[0] >> 3) << 17);
             const uint32_t idesc_b = idesc0 | ((uint32_t)(U.n[1] >> 3) << 17);
             const uint64_t to_b = U.n[0] / 2 * (BT * 2) / 16;  // from one Q tile to the other
-            for (int a = 0; a < accs && ok; ++a)
-              ok = wait(bar_acc_empty + 8 * ((acc + a) & 1), ((uint32_t)((acc + a) >> 1) & 1u) ^ 1u,
-                        kWaitLimitNs);
-            if (!ok) break;
-            tc_fence_after();
-            for (int b = 0; b < U.blocks; ++b) {
-              if (b == U.blocks - 1) next = take(seq + 1, N);
-              ok = wait(bar_full + 8 * ring.bar, ring.phase, kWaitLimitNs);
+            const int piece = kLong ? kJoinBlocks : U.blocks;  // of one sum
+            for (int b0 = 0; ok && b0 < U.blocks; b0 += piece) {
+              const int b1 = min(U.blocks, b0 + piece);
+              for (int a = 0; a < accs && ok; ++a)
+                ok = wait(bar_acc_empty + 8 * ((acc + a) & 1), ((uint32_t)((acc + a) >> 1) & 1u) ^ 1u,
+                          kWaitLimitNs);
               if (!ok) break;
               tc_fence_after();
-              const uint32_t sp = s_ring + ring.place(bytes);
-              const uint64_t dp = operand_desc<kPMn>(sp), dq = operand_desc<kQMn>(sp + kPBytes);
-              const int steps = b == U.blocks - 1 ? (U.rem + 15) >> 4 : BT / 16;
-              multiply(tmem + 256 * (acc & 1), dp, dq, idesc_a, steps, b != 0);
-              if (accs == 2) multiply(tmem + 256 * ((acc + 1) & 1), dp, dq + to_b, idesc_b, steps, b != 0);
-              tc_commit_pair_mc(bar_empty + 8 * ring.bar, kBoth);
-              ring.next_block();
+              for (int b = b0; b < b1; ++b) {
+                if (b == U.blocks - 1) next = take(seq + 1, N);
+                ok = wait(bar_full + 8 * ring.bar, ring.phase, kWaitLimitNs);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sp = s_ring + ring.place(bytes);
+                const uint64_t dp = operand_desc<kPMn>(sp), dq = operand_desc<kQMn>(sp + kPBytes);
+                const int steps = b == U.blocks - 1 ? (U.rem + 15) >> 4 : BT / 16;
+                multiply(tmem + 256 * (acc & 1), dp, dq, idesc_a, steps, b != b0);
+                if (accs == 2)
+                  multiply(tmem + 256 * ((acc + 1) & 1), dp, dq + to_b, idesc_b, steps, b != b0);
+                tc_commit_pair_mc(bar_empty + 8 * ring.bar, kBoth);
+                ring.next_block();
+              }
+              if (!ok) break;
+              for (int a = 0; a < accs; ++a, ++acc) tc_commit_pair_mc(bar_acc_full + 8 * (acc & 1), kBoth);
             }
-            if (!ok) break;
-            for (int a = 0; a < accs; ++a, ++acc) tc_commit_pair_mc(bar_acc_full + 8 * (acc & 1), kBoth);
           }
         }
         // so do the odd CTA's last releases
@@ -825,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int segment = -1;
       for (int u = cluster_id_x(); ok && u < units; u += cluster_count_x())
-        ok = push(get_unit<kMode, kF32>(P, S.table, u, p_tiles, segment));
+        ok = push(get_unit<kMode, kF32, kLong>(P, S.table, u, p_tiles, segment));
       if (ok) {
         Unit end = {};
         end.end = 1;
@@ -882,6 +910,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lead_acc_empty = mapa_shared(bar_acc_empty, 0);
     uint8_t *stage0_ptr = smem + kRing + (warp - 4) * stage_bytes(kMode, kF32);
     const uint32_t stage0 = smem_u32(stage0_ptr);
+    // A rounded block of 32 x 32 to the gradient's q.. x p..; what passes the extents is left out.
+    auto stage_out = [&](const uint32_t *w, int q, int p, int z) {
+      if (elect_one()) bulk_wait_read<0>();  // the block's last copy has left it
+      __syncwarp();
+      stage_rows(w, stage0, lane);
+      fence_async_shared();
+      __syncwarp();
+      if (p < P.np && elect_one()) {
+        tma_store(&M.out, stage0, p, q, z);
+        bulk_commit();
+      }
+    };
     int turn = 0;
     int acc = 0;
     bool ok = true;
@@ -962,6 +1002,59 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           turn = block(done);
         }
+      } else if (kLong && (kMode != kGrad || U.join)) {
+        // Partial sums of one accumulator's columns, joined in the registers that load_columns
+        // (gradient) or a lane's 32 columns (forward, trans) give.
+        constexpr int kPart = kMode == kGrad ? 8 : 16;
+        float sum[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[i][j] = 0.0f;
+        const int sums = (U.blocks + kJoinBlocks - 1) / kJoinBlocks, nq = U.nq;
+        for (int s = 0; s < sums; ++s, ++acc) {
+          const int buf = acc & 1;
+          if (!wait_warp(bar_acc_full + 8 * buf, (uint32_t)(acc >> 1) & 1u, unit_limit)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = 32 * (half + 2 * i);
+            if (c < nq) {
+#pragma unroll
+              for (int h = 0; h < 32; h += kPart) {  // parts that leave the sums in registers
+                uint32_t v[kPart];
+                if constexpr (kMode == kGrad)
+                  tmem_ld_16x256b_x2(t_lane + 256 * buf + c + (h & 8 ? 16 : 0) + ((uint32_t)(h & 16) << 16), v);
+                else
+                  tmem_ld_x16(t_lane + 256 * buf + c + h, v);
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < kPart; ++j) sum[i][h + j] += __uint_as_float(v[j]);
+              }
+            }
+          }
+          release(buf);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = 32 * (half + 2 * i);
+          if (c >= nq) continue;
+          uint32_t v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(sum[i][j]);
+          if constexpr (kMode == kGrad) {
+            uint32_t w[16];
+            round_columns<O>(v, false, w);
+            stage_out(w, U.q0 + c, pw, U.z);
+          } else {
+            store_columns<O>(v, static_cast<uint16_t *>(P.out) + pw + (int64_t)(U.q0 + c) * P.np, P.np,
+                             nq - c, pw + lane < P.np, lane);
+          }
+        }
       } else if constexpr (kMode == kGrad) {
         for (int g = 0; g < U.tiles; ++g) {
           const int buf = acc & 1, q0 = U.q0 + BQ * g, nq = min(BQ, U.nq - BQ * g);
@@ -987,15 +1080,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               load_columns(t_lane + 256 * buf + c + 64, v);  // on their way during the stores
             else if (some)
               release(buf);
-            if (elect_one()) bulk_wait_read<0>();  // the block's last copy has left it
-            __syncwarp();
-            stage_rows(w, stage0, lane);
-            fence_async_shared();
-            __syncwarp();
-            if (pw < P.np && elect_one()) {  // what passes the extents is left out
-              tma_store(&M.out, stage0, pw, q0 + c, U.z);
-              bulk_commit();
-            }
+            stage_out(w, q0 + c, pw, U.z);
           }
         }
       } else {
@@ -1092,12 +1177,12 @@ int check_common(const moe_segments &seg, int n, int k, int type) {
 bool off16(const void *p) { return (uintptr_t)p % 16 != 0; }
 
 // max_units: no more units than this (the grid need not be larger).
-template <int kMode, class O>
+template <int kMode, class O, bool kLong = false>
 int launch(const Maps &maps, const GroupedParams &P, int64_t max_units, int num_sms, void *stream) {
   static int max_clusters[kMaxDevices] = {};
   const int dev = device_slot();
   if (dev < 0) return dev;
-  auto kernel = grouped_kernel<kMode, O>;
+  auto kernel = grouped_kernel<kMode, O, kLong>;
   const int sms = num_sms > 0 ? num_sms : device_sm_count();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(sms / 2 > 0 ? sms / 2 * 2 : 2));
@@ -1148,6 +1233,7 @@ extern "C" int moe_grouped_gemm(const moe_ggemm_args *a, void *stream) {
   P.np = a->trans ? a->k : a->n;
   P.nt = a->trans ? a->n : a->k;
   P.bf16 = a->type == MOE_TYPE_BF16;
+  P.longest = P.bf16 ? kLongestBf16 : kLongestF16;
   P.out = a->out;
   P.p_blocked = a->k % BT == 0;
   Maps maps = {};
@@ -1155,16 +1241,21 @@ extern "C" int moe_grouped_gemm(const moe_ggemm_args *a, void *stream) {
   bool ok = a->trans ? map_mn_major(&maps.p, a->w, E, n, k, 2) : map_k_major(&maps.p, a->w, E, n, k, 128);
   for (int i = 0; i < 8; ++i) ok = ok && map_k_major(&maps.q[i], a->x, 1, rows, P.nt, 16 * (i + 1));
   if (!ok) return MOE_ERR_CUDA;
-  // row tiles: a full one per 512 rows, and one started in every segment that has rows
+  // row tiles: a full one per 512 rows (256), and one started in every segment that has rows
+  const bool longer = P.nt > P.longest;
   const int64_t started = a->seg.E < a->seg.rows ? a->seg.E : a->seg.rows;
-  const int64_t max_units = (a->seg.rows / kWide + started) * ((P.np + BP - 1) / BP);
+  const int64_t max_units = (a->seg.rows / (longer ? BQ : kWide) + started) * ((P.np + BP - 1) / BP);
   if (max_units > INT32_MAX) return MOE_ERR_UNSUPPORTED;
-  const bool bf = P.bf16;
-  if (a->trans)
-    return bf ? launch<kTrans, __nv_bfloat16>(maps, P, max_units, a->num_sms, stream)
-              : launch<kTrans, __half>(maps, P, max_units, a->num_sms, stream);
-  return bf ? launch<kFwd, __nv_bfloat16>(maps, P, max_units, a->num_sms, stream)
-            : launch<kFwd, __half>(maps, P, max_units, a->num_sms, stream);
+  auto run = [&](auto mode, auto value) {
+    constexpr int kMode = decltype(mode)::value;
+    using O = decltype(value);
+    return longer ? launch<kMode, O, true>(maps, P, max_units, a->num_sms, stream)
+                  : launch<kMode, O>(maps, P, max_units, a->num_sms, stream);
+  };
+  const std::integral_constant<int, kFwd> fwd;
+  const std::integral_constant<int, kTrans> trans;
+  if (a->trans) return P.bf16 ? run(trans, __nv_bfloat16()) : run(trans, __half());
+  return P.bf16 ? run(fwd, __nv_bfloat16()) : run(fwd, __half());
 }
 
 extern "C" int moe_grouped_wgrad(const moe_wgrad_args *a, void *stream) {
@@ -1181,6 +1272,7 @@ extern "C" int moe_grouped_wgrad(const moe_wgrad_args *a, void *stream) {
   P.np = a->k;
   P.nq = a->n;
   P.bf16 = a->type == MOE_TYPE_BF16;
+  P.longest = P.bf16 ? kLongestBf16 : kLongestF16;
   P.out = a->out;
   P.accumulate = a->accumulate != 0;
   P.p_blocked = a->k % BT == 0;
@@ -1203,6 +1295,9 @@ extern "C" int moe_grouped_wgrad(const moe_wgrad_args *a, void *stream) {
   if (max_units > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (f32)
     return launch<kGrad, float>(maps, P, max_units, a->num_sms, stream);
+  if (a->seg.rows > P.longest)  // some segment may be
+    return P.bf16 ? launch<kGrad, __nv_bfloat16, true>(maps, P, max_units, a->num_sms, stream)
+                  : launch<kGrad, __half, true>(maps, P, max_units, a->num_sms, stream);
   return P.bf16 ? launch<kGrad, __nv_bfloat16>(maps, P, max_units, a->num_sms, stream)
                 : launch<kGrad, __half>(maps, P, max_units, a->num_sms, stream);
 }

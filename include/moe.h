@@ -494,7 +494,9 @@ typedef struct moe_segments {
  *     gradient of that product with respect to its input, or the forward product of
  *     weights stored [k][n]);
  * for every row r of expert e's segment, w [E][n][k]; one rounding to the 16-bit type
- * at the end.  num_sms: CTAs of the persistent grid (0: every SM).
+ * at the end.  The tensor core adds up to 16384 terms (fp16) or 131072 (bf16), truncating:
+ * at most about 1/25 of that rounding; longer sums are joined from partial sums of 4096 by
+ * binary32 additions.  num_sms: CTAs of the persistent grid (0: every SM).
  * Errors, before any launch: MOE_ERR_INVALID for a null pointer, a bad type or size, or
  * x, w or out not 16-byte aligned; MOE_ERR_UNSUPPORTED for n or k not a multiple of 8
  * or sizes outside the limits above.  rows == 0 enqueues nothing.
@@ -515,9 +517,9 @@ int moe_grouped_gemm(const moe_ggemm_args *args, void *stream);
 /*
  * Weight gradient of the grouped product: dw[e][j][i] = sum over the rows r of expert
  * e's segment of dy[r][j] * x[r][i], dy [rows][n], x [rows][k], out [E][n][k].
- *   out_type: `type` (one rounding at the end) or MOE_TYPE_F32.  accumulate != 0 (with
- *   MOE_TYPE_F32): out += dw (gradients over several micro-batches); experts without
- *   rows then keep their values, and otherwise get zeros.
+ *   out_type: `type` (one rounding at the end; long segments as in moe_grouped_gemm) or
+ *   MOE_TYPE_F32.  accumulate != 0 (with MOE_TYPE_F32): out += dw (gradients over several
+ *   micro-batches); experts without rows then keep their values, and otherwise get zeros.
  *   With MOE_TYPE_F32 partial sums of at most 512 rows are joined by binary32 additions
  *   (the tensor core's own accumulation truncates, which would show over long segments).
  *   The order of the additions is fixed: the same inputs give the same bits.

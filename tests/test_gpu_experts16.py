@@ -198,6 +198,55 @@ def test_wgrad_in_binary32_stays_exact_over_long_segments(dev):
     assert float((got - ref).norm() / ref.norm()) <= (512 / 16 + 20000 / 512) * 2.0 ** -24
 
 
+@pytest.mark.parametrize("dtype,t", [(F16, 2 ** 21), (BF16, 2 ** 23)])
+def test_long_sums_round_once(dev, dtype, t):
+    """Sums of one sign over millions of terms: partial sums of 4096 (256 truncating
+    instructions) and one addition for each keep the error below the 16-bit rounding, which
+    truncation throughout would pass several times."""
+    gen = torch.Generator("cuda").manual_seed(24)
+    a = normal(gen, t, 8, dtype=dtype, scale=2.0 ** -6).abs()
+    b = normal(gen, t, 16, dtype=dtype, scale=2.0 ** -8).abs()
+    ref = torch.zeros(8, 16, dtype=torch.float64, device=dev)
+    for at in range(0, t, 2 ** 20):
+        ref += a[at:at + 2 ** 20].double().t() @ b[at:at + 2 ** 20].double()
+    slack = (4096 / 16 + t / 4096 + 8) * ADD * ref
+    check_close(api.grouped_wgrad(a, b, i32([t]))[0], ref, slack, dtype)
+    at, bt = a.t().contiguous(), b.t().contiguous()          # [8][t], [16][t]
+    check_close(api.grouped_gemm(at, bt[None], i32([8])), ref, slack, dtype)
+    check_close(api.grouped_gemm(bt, a[None], i32([16]), trans=True), ref.t(), slack.t(), dtype)
+
+
+@pytest.mark.parametrize("sms", [0, 4])
+def test_long_sums_beside_short_ones(dev, sms):
+    """Segments (gradient) and contractions (forward, trans) on both sides of the longest sum
+    that is not joined, several units a pair, NaN in the padding.  Whole numbers whose sums
+    binary32 holds: equality."""
+    gen = torch.Generator("cuda").manual_seed(25)
+
+    def whole(*shape):
+        return torch.randint(-2, 3, shape, generator=gen, device="cuda").to(F16)
+    counts, n, k = [16385, 0, 37, 16384, 20011, 400, 4096, 33000], 520, 328
+    starts, rows = starts_of(counts, 64), rows_of(counts, 64)
+    dy = torch.full((rows, n), float("nan"), dtype=F16, device=dev)
+    x = torch.full((rows, k), float("nan"), dtype=F16, device=dev)
+    want = torch.zeros(len(counts), n, k, device=dev)
+    for e, (m, s) in enumerate(zip(counts, starts)):
+        dy[s:s + m], x[s:s + m] = whole(m, n), whole(m, k)
+        want[e] = (dy[s:s + m].double().t() @ x[s:s + m].double()).float()
+    for _ in range(3):
+        assert torch.equal(api.grouped_wgrad(dy, x, i32(counts), align=64, num_sms_=sms), want.to(F16))
+        assert torch.equal(api.grouped_wgrad(dy, x, i32(counts), align=64, out_dtype=F32, num_sms_=sms), want)
+    counts = [3, 300, 0, 513, 256, 257]
+    for t in (16384, 16392, 20520):
+        w, x = whole(len(counts), 264, t), whole(sum(counts), t)
+        w2 = w.transpose(1, 2).contiguous()
+        want = torch.cat([x[s:s + m].double() @ w[e].double().t()
+                          for e, (m, s) in enumerate(zip(counts, starts_of(counts)))]).float().to(F16)
+        for _ in range(3):
+            assert torch.equal(api.grouped_gemm(x, w, i32(counts), num_sms_=sms), want)
+            assert torch.equal(api.grouped_gemm(x, w2, i32(counts), trans=True, num_sms_=sms), want)
+
+
 def test_wgrad_is_the_gradient_of_the_product(dev):
     """Central differences of L = sum(c * y), y the 64-bit forward, at random weights and
     inputs against grouped_wgrad and grouped_gemm(trans)."""
