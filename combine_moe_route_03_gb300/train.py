@@ -58,13 +58,17 @@ class ExpertTrainer:
         return d["A"].view(torch.bfloat16), d
 
     def forward(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor) -> torch.Tensor:
-        """x bf16 [B][H], topk_idx and topk_w [B][K] (as api.route gives them) -> bf16 [B][H]."""
+        """x bf16 [B][H], topk_idx and topk_w [B][K] (as api.route gives them) -> bf16 [B][H].
+        A pair whose expert index lies outside [0, N) is left out, as dispatch and combine do:
+        it adds nothing, and the gradient of its weight is 0."""
         rows_x, d = self._dispatch(x, topk_idx)
         seg = dict(counts=d["counts"], align=ALIGN, status=self.status)
-        row_of = d["row_of"]
-        at = row_of.reshape(-1).long()
-        row_w = torch.zeros(d["rows"], dtype=torch.float32, device=x.device)
+        row_of, rows = d["row_of"], d["rows"]
+        # pairs left out (row -1) share one entry behind the rows
+        at = torch.where(row_of < 0, rows, row_of).reshape(-1).long()
+        row_w = torch.zeros(rows + 1, dtype=torch.float32, device=x.device)
         row_w[at] = topk_w.reshape(-1)
+        row_w = row_w[:rows]
         gu = api.grouped_gemm(rows_x, self.W13, **seg)
         h = api.swiglu(gu, row_w=row_w, **seg)
         y = api.grouped_gemm(h, self.W2, **seg)
@@ -84,7 +88,8 @@ class ExpertTrainer:
         self._fresh = False
         api.grouped_wgrad(dy, h, out=self.grads[1], **more)
         dh = api.grouped_gemm(dy, self.W2, trans=True, **seg)
-        dgu, drow_w = api.swiglu_backward(gu, dh, row_w=row_w, dgu=gu, **seg)
+        drow_w = torch.zeros(row_w.numel() + 1, dtype=torch.float32, device=dy.device)
+        dgu, _ = api.swiglu_backward(gu, dh, row_w=row_w, dgu=gu, drow_w=drow_w[:-1], **seg)
         api.grouped_wgrad(dgu, rows_x, out=self.grads[0], **more)
         dx = api.grouped_gemm(dgu, self.W13, trans=True, **seg)
         return api.combine(dx, row_of, ones, status=self.status), drow_w[at].view(ones.shape)

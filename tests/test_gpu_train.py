@@ -3,7 +3,7 @@ use over several micro-batches and steps."""
 import pytest
 import torch
 
-from combine_moe_route_03_gb300 import api, configs, train
+from combine_moe_route_03_gb300 import _lib, api, configs, train
 
 pytestmark = pytest.mark.gpu
 
@@ -48,6 +48,26 @@ def test_forward_and_gradients_match_autograd(dev):
     dx, dw = t.backward(dout)
     want = reference(SMALL, W13, W2, x, dout, idx, w)
     assert api.read_status(t.status) == 0
+    assert off(out, want[0]) <= OUT
+    for got, ref in zip((dx, dw, t.grads[0], t.grads[1]), want[1:]):
+        assert off(got, ref) <= GRAD
+
+
+def test_pairs_left_out_have_no_gradient(dev):
+    """Expert indices outside [0, N), one token's all of them, over memory that held NaN."""
+    W13, W2, x, dout, idx, w = make(SMALL, 2)
+    idx = idx.clone()
+    idx[3, 1], idx[10, 0], idx[76, 2] = -1, SMALL.N, -7
+    idx[20] = -1
+    out_of = (idx < 0) | (idx >= SMALL.N)
+    t = train.ExpertTrainer(SMALL, W13, W2)
+    used = [torch.full((2 ** n,), 0xFF, dtype=torch.uint8, device=dev) for n in range(10, 24) for _ in range(4)]
+    del used
+    out = t.forward(x, idx, w)
+    dx, dw = t.backward(dout)
+    want = reference(SMALL, W13, W2, x, dout, idx, w)
+    assert api.read_status(t.status) == _lib.STATUS_BAD_INDEX
+    assert not bool(dw[out_of].any()) and not bool(out[20].any()) and not bool(dx[20].any())
     assert off(out, want[0]) <= OUT
     for got, ref in zip((dx, dw, t.grads[0], t.grads[1]), want[1:]):
         assert off(got, ref) <= GRAD
