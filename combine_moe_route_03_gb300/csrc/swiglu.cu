@@ -7,9 +7,11 @@
 // number of rows), so dw is a reduction inside it: lanes in their order, then warps in
 // theirs, the same bits every time.  The rows of the segments are numbered through (a
 // table of the segments in shared memory maps the number to the row), so padding costs
-// nothing and no row is tested.  65536 rows of I = 2048: forward 134 us (6.0 TB/s),
-// backward with dw 213 us (6.3 TB/s), where a copy runs at 6.8.
+// nothing and no row is tested.  65536 rows of I = 2048: forward 130 us (6.2 TB/s),
+// backward with dw 212 us (6.3 TB/s), where a copy runs at 6.8.
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "segments.cuh"
 
@@ -54,17 +56,40 @@ struct SwigluParams {
   float *drow_w;
 };
 
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// Gates below -87: 1 + e^-g passes the divisors that __fdividef takes (2^126), and soon
+// binary32 itself; the sigmoid is e^g to the last bit there.  A large u or w brings the
+// products back into range; what stays below 2^-100 counts as zero.  kLow: with such gates.
+// Eight values are tested for them at once, as whole numbers, and computed one by one if there
+// is one (65536 rows of 2048: 130 us; selected value by value 158).
+constexpr float kLowGate = -87.0f;
+template <bool kLow>
+__device__ __forceinline__ float sigmoid(float g) {
+  if (kLow && g < kLowGate) return __expf(g);
+  return __fdividef(1.0f, 1.0f + __expf(-g));
+}
+template <bool kLow>
+__device__ __forceinline__ float settled(float r, float g) {
+  return kLow && g < kLowGate && fabsf(r) < 0x1p-100f ? 0.0f : r;
+}
+// Whether any of 8 gates is that low: its bits, a number without sign, are above -87's.
+template <class T>
+__device__ __forceinline__ bool any_low(const Vec8<T> &g) {
+  constexpr unsigned kBits = std::is_same<T, __half>::value ? 0xd570u : 0xc2aeu;
+  const unsigned m = __vmaxu2(__vmaxu2(g.q.x, g.q.y), __vmaxu2(g.q.z, g.q.w));
+  return (m >> 16) > kBits || (m & 0xffffu) > kBits;
+}
 
 // One value: forward (h), or backward (dg, du and the term of dw).
+template <bool kLow>
 __device__ __forceinline__ float forward_one(float g, float u, float w) {
-  return w * (g * sigmoid(g)) * u;
+  return settled<kLow>(w * (g * sigmoid<kLow>(g)) * u, g);
 }
+template <bool kLow>
 __device__ __forceinline__ float backward_one(float g, float u, float dh, float w, float &dg,
                                               float &du) {
-  const float s = sigmoid(g), a = g * s, wd = w * dh;
-  dg = wd * u * (s + a * (1.0f - s));
-  du = wd * a;
+  const float s = sigmoid<kLow>(g), a = g * s, wd = w * dh;
+  dg = settled<kLow>(wd * u * (s + a * (1.0f - s)), g);
+  du = settled<kLow>(wd * a, g);
   return dh * a * u;
 }
 
@@ -97,6 +122,17 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluParams P) 
     const T *g_row = gu + (size_t)r * 2 * I, *dh_row = dhp + (size_t)r * I;
     T *o_row = outp + (size_t)r * (kBackward ? 2 * I : I);
     float sum = 0.0f;
+    auto one = [&](int j) {
+      const float gf = to_f32(g_row[j]), uf = to_f32(g_row[I + j]);
+      if constexpr (kBackward) {
+        float dg, du;
+        sum += backward_one<true>(gf, uf, to_f32(dh_row[j]), w, dg, du);
+        o_row[j] = from_f32<T>(dg);
+        o_row[I + j] = from_f32<T>(du);
+      } else {
+        o_row[j] = from_f32<T>(forward_one<true>(gf, uf, w));
+      }
+    };
 #pragma unroll 4
     for (int j = t * V; j < I; j += kRow * V) {
       if constexpr (kVec) {
@@ -104,30 +140,27 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluParams P) 
         g.q = __ldcs(reinterpret_cast<const uint4 *>(g_row + j));
         u.q = __ldcs(reinterpret_cast<const uint4 *>(g_row + I + j));
         if constexpr (kBackward) d.q = __ldcs(reinterpret_cast<const uint4 *>(dh_row + j));
+        if (any_low(g)) {
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) one(j + i);
+          continue;
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float gf = to_f32(g.t[i]), uf = to_f32(u.t[i]);
           if constexpr (kBackward) {
             float dg, du;
-            sum += backward_one(gf, uf, to_f32(d.t[i]), w, dg, du);
+            sum += backward_one<false>(gf, uf, to_f32(d.t[i]), w, dg, du);
             o.t[i] = from_f32<T>(dg);
             o2.t[i] = from_f32<T>(du);
           } else {
-            o.t[i] = from_f32<T>(forward_one(gf, uf, w));
+            o.t[i] = from_f32<T>(forward_one<false>(gf, uf, w));
           }
         }
         *reinterpret_cast<uint4 *>(o_row + j) = o.q;
         if constexpr (kBackward) *reinterpret_cast<uint4 *>(o_row + I + j) = o2.q;
       } else {
-        const float gf = to_f32(g_row[j]), uf = to_f32(g_row[I + j]);
-        if constexpr (kBackward) {
-          float dg, du;
-          sum += backward_one(gf, uf, to_f32(dh_row[j]), w, dg, du);
-          o_row[j] = from_f32<T>(dg);
-          o_row[I + j] = from_f32<T>(du);
-        } else {
-          o_row[j] = from_f32<T>(forward_one(gf, uf, w));
-        }
+        one(j);
       }
     }
     if (kBackward && P.drow_w) {

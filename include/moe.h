@@ -549,9 +549,10 @@ int moe_grouped_wgrad(const moe_wgrad_args *args, void *stream);
  *   moe_swiglu_backward: out [rows][2I] = (w dh u sigmoid(g) (1 + g sigmoid(-g)), w dh a)
  *     and, with drow_w non-NULL, drow_w[r] = sum_j dh a u (the gradient of w[r]),
  *     for dh [rows][I] the gradient of the activation.
- * Computed in binary32, rounded once.  drow_w is summed in a fixed order.  The
- * backward's out may be gu itself.  I >= 1; any alignment of the element type (16-byte
- * aligned tensors with I % 8 == 0 take the fast path).  Errors: MOE_ERR_INVALID for a
+ * Computed in binary32, rounded once; for gates below -87, whose sigmoid is below or next
+ * to binary32's smallest normal number, results below 2^-100 are zero.  drow_w is summed in
+ * a fixed order.  The backward's out may be gu itself.  I >= 1; any alignment of the element
+ * type (16-byte aligned tensors with I % 8 == 0 take the fast path).  Errors: MOE_ERR_INVALID for a
  * null pointer, a bad type or size; MOE_ERR_UNSUPPORTED outside the limits of the
  * segments, or I > 2^24.
  */

@@ -481,6 +481,30 @@ def test_swiglu_of_unaligned_tensors_and_extreme_gates(dev):
     assert torch.isnan(h[:2]).all() and h[2] == float("inf") and h[3] == -float("inf")
 
 
+@pytest.mark.parametrize("I", [1, 64])
+def test_swiglu_of_very_negative_gates(dev, I):
+    """Gates whose sigmoid is near binary32's smallest values, times an up value and a row
+    weight that bring the product back: down to -87 the sigmoid is a normal number, with e^g's
+    relative error of about |g| roundings; below, the subnormal's own rounding (2^-150) adds.
+    What stays below 2^-100 for such a gate counts as zero."""
+    g = -torch.arange(80.0, 100.0, 0.5, device=dev).to(BF16)
+    gu = torch.stack((g, torch.full_like(g, 1e30)), 1).repeat_interleave(I, dim=1)
+    w = torch.full((len(g),), 3.0, device=dev)
+    dh = torch.ones(len(g), I, dtype=BF16, device=dev)
+    gd, u = gu[:, :I].double(), gu[:, I:].double()
+    s = torch.sigmoid(gd)
+    rel = (gd.abs() + 16) * ADD + 2.0 ** -149 / s
+    h = 3 * gd * s * u
+    check_close(api.swiglu(gu, row_w=w), h, rel * h.abs(), BF16)
+    dgu, dw = api.swiglu_backward(gu, dh, row_w=w)
+    dg = 3 * u * s * (1 + gd * torch.sigmoid(-gd))
+    check_close(dgu[:, :I], dg, rel * 3 * u * s * (1 + gd.abs()), BF16)
+    check_close(dgu[:, I:], 3 * gd * s, rel * (3 * gd * s).abs() + 2.0 ** -100, BF16)
+    check_close(dw, (gd * s * u).sum(1), ((rel + (I + 64) * ADD / 2) * (gd * s * u).abs()).sum(1), F32)
+    h16 = api.swiglu(torch.stack((g, torch.ones_like(g)), 1).to(F16))     # under fp16's range: zero
+    assert not bool(h16.any())
+
+
 def test_swiglu_gradient_is_the_difference_of_the_forward(dev):
     gen = torch.Generator("cuda").manual_seed(12)
     rows, I = 4, 16
