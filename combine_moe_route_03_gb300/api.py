@@ -525,8 +525,8 @@ class AdamW:
 
     The moments live in flat buffers, each tensor's piece starting at a multiple of 256
     values (``offsets``): ``m`` and ``v``, or ``m_code`` / ``r_code`` with ``m_scale`` /
-    ``r_scale`` per 256 values.  The parameters' and copies' addresses are taken once:
-    keep the tensors.  ``lr``, ``betas``, ``eps`` and ``weight_decay`` may be changed
+    ``r_scale`` per 256 values.  The addresses of parameters, copies and moments are taken
+    once: a step refuses tensors that have another storage, size or type since.  ``lr``, ``betas``, ``eps`` and ``weight_decay`` may be changed
     between steps; ``steps`` counts the steps taken."""
 
     BLOCK = 256
@@ -568,12 +568,27 @@ class AdamW:
                 t.m, t.v = ptr(self.m_code) + o, ptr(self.r_code) + o
                 t.m_scale = ptr(self.m_scale) + o // self.BLOCK * 4
                 t.r_scale = ptr(self.r_scale) + o // self.BLOCK * 4
+        self._places = [self._place(t) for t in self._held()]
+
+    def _held(self) -> list:
+        """Every tensor whose address the table holds."""
+        moments = ((self.m, self.v) if self.state_bits == 32 else
+                   (self.m_code, self.r_code, self.m_scale, self.r_scale))
+        return [*self.params, *(c for c in self.copies if c is not None), *moments]
+
+    @staticmethod
+    def _place(t: torch.Tensor) -> tuple:
+        return t.data_ptr(), t.numel(), t.dtype, t.is_contiguous()
 
     def step(self, grads, grad_scale: torch.Tensor | None = None, stream=None) -> None:
         """One step with one gradient (bf16, fp16 or fp32, the parameter's shape) per
         parameter; grad_scale: fp32 device scalar that multiplies every gradient."""
         if len(grads) != len(self.params):
             raise ValueError(f"{len(self.params)} gradients expected, got {len(grads)}")
+        place = self._place
+        if [place(t) for t in self._held()] != self._places:
+            raise ValueError("the storage, size and type that parameters, copies and moments had "
+                             "when this AdamW was made expected")
         addresses, s = ptrs(*grads)
         for t, p, g, a in zip(self._table, self.params, grads, addresses):
             kind = _TYPES.get(g.dtype)

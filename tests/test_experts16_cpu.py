@@ -162,3 +162,51 @@ def test_binding_refuses_host_tensors_and_shapes(L):
                  lambda: api.AdamW([])):
         with pytest.raises(ValueError, match="expected"):
             call()
+
+
+class Calls:
+    """Stands in for the library: records the calls, touches nothing."""
+
+    def __init__(self):
+        self.names = []
+
+    def __getattr__(self, name):
+        return lambda *a: self.names.append(name) or 0
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The binding over host tensors and a library that only records."""
+    c = Calls()
+    address = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    monkeypatch.setattr(api, "load", lambda: c)
+    monkeypatch.setattr(api, "ptr", address)
+    monkeypatch.setattr(api, "ptrs", lambda *ts: ([address(t) for t in ts], 0))
+    return c
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_refuses_tensors_that_moved(calls, bits):
+    """A parameter, copy or moment whose storage was replaced: the step would write where it
+    lay before."""
+    def new():
+        return api.AdamW([torch.zeros(3, 5), torch.zeros(300)], state_bits=bits,
+                         copies=[torch.zeros(3, 5, dtype=torch.bfloat16), None])
+    grads = [torch.zeros(3, 5), torch.zeros(300)]
+
+    def data(t, value):
+        t.data = value
+    name = "v" if bits == 32 else "r_scale"
+    for move in (lambda o: data(o.params[1], torch.zeros(300)),
+                 lambda o: data(o.params[0], o.params[0].data.view(5, 3).t()),
+                 lambda o: data(o.params[1], o.params[1].data[:200]),
+                 lambda o: data(o.copies[0], torch.zeros(3, 5, dtype=torch.bfloat16)),
+                 lambda o: data(o.copies[0], o.copies[0].data.view(torch.float16)),
+                 lambda o: setattr(o, name, getattr(o, name).clone())):
+        opt = new()
+        opt.step(grads)
+        assert calls.names.pop() == "moe_adamw" and opt.steps == 1
+        move(opt)
+        with pytest.raises(ValueError, match="expected"):
+            opt.step([torch.zeros(p.shape) for p in opt.params])
+        assert calls.names == [] and opt.steps == 1
