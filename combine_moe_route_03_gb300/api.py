@@ -589,6 +589,9 @@ class AdamW:
         if [place(t) for t in self._held()] != self._places:
             raise ValueError("the storage, size and type that parameters, copies and moments had "
                              "when this AdamW was made expected")
+        for g in grads:
+            if not isinstance(g, torch.Tensor):
+                raise TypeError("gradient: a torch tensor is required (one for each parameter)")
         addresses, s = ptrs(*grads)
         for t, p, g, a in zip(self._table, self.params, grads, addresses):
             kind = _TYPES.get(g.dtype)

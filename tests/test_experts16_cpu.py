@@ -210,3 +210,11 @@ def test_adamw_refuses_tensors_that_moved(calls, bits):
         with pytest.raises(ValueError, match="expected"):
             opt.step([torch.zeros(p.shape) for p in opt.params])
         assert calls.names == [] and opt.steps == 1
+
+
+def test_adamw_refuses_gradients_that_are_no_tensors(calls):
+    opt = api.AdamW([torch.zeros(4), torch.zeros(5)])
+    for bad in (None, 1.0, [0.0] * 5):
+        with pytest.raises(TypeError, match="torch tensor"):
+            opt.step([torch.zeros(4), bad])
+    assert calls.names == [] and opt.steps == 0
