@@ -585,8 +585,8 @@ class AdamW:
         parameter; grad_scale: fp32 device scalar that multiplies every gradient."""
         if len(grads) != len(self.params):
             raise ValueError(f"{len(self.params)} gradients expected, got {len(grads)}")
-        place = self._place
-        if [place(t) for t in self._held()] != self._places:
+        place, held = self._place, self._held()
+        if [place(t) for t in held] != self._places:
             raise ValueError("the storage, size and type that parameters, copies and moments had "
                              "when this AdamW was made expected")
         for g in grads:
@@ -606,7 +606,7 @@ class AdamW:
         cfg = AdamwCfg(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
                        self.steps + 1, self.state_bits, ptr(grad_scale))
         check(load().moe_adamw(ctypes.byref(cfg), self._table, len(self.params),
-                               _on(stream, s, *grads, grad_scale)), "moe_adamw")
+                               _on(stream, s, *grads, grad_scale, *held)), "moe_adamw")
         self.steps += 1
 
     def state(self, stream=None):
@@ -618,8 +618,8 @@ class AdamW:
                 for _ in range(2))
         (mc, ms, rc, rs, pm, pv), s = ptrs(self.m_code, self.m_scale, self.r_code, self.r_scale,
                                            m, v)
-        check(load().moe_adamw_decode(self.numel, mc, ms, rc, rs, pm, pv, _on(stream, s, m, v)),
-              "moe_adamw_decode")
+        check(load().moe_adamw_decode(self.numel, mc, ms, rc, rs, pm, pv,
+                                      _on(stream, s, m, v, *self._held())), "moe_adamw_decode")
         return m, v
 
     def load_state(self, m: torch.Tensor, v: torch.Tensor, steps: int, stream=None) -> None:
@@ -627,14 +627,14 @@ class AdamW:
         for t, what in ((m, "m"), (v, "v")):
             _expect(t, what, (torch.float32,), (self.numel,))
         if self.state_bits == 32:
-            _ordered(stream, m, v)
+            _ordered(stream, m, v, *self._held())
             with torch.cuda.stream(stream):
                 self.m.copy_(m)
                 self.v.copy_(v)
         else:
             check(load().moe_adamw_encode(self.numel, ptr(m), ptr(v), ptr(self.m_code),
                                           ptr(self.m_scale), ptr(self.r_code),
-                                          ptr(self.r_scale), _ordered(stream, m, v)),
+                                          ptr(self.r_scale), _ordered(stream, m, v, *self._held())),
                   "moe_adamw_encode")
         self.steps = steps
 

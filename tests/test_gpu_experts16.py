@@ -753,6 +753,44 @@ def test_operators_on_another_stream(dev):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_on_another_stream_keeps_what_it_holds(dev, bits):
+    """The object and its copy dropped right after a step and a read-out on a stream that is
+    still busy: their memory is not handed out before those are done."""
+    side, n = torch.cuda.Stream(), 1 << 20
+    gen = torch.Generator("cuda").manual_seed(26)
+    p0, g = torch.randn(n, generator=gen, device=dev), torch.randn(n, generator=gen, device=dev)
+    m0, v0 = torch.randn(n, generator=gen, device=dev), torch.rand(n, generator=gen, device=dev)
+
+    def make(p):
+        opt = api.AdamW([p], state_bits=bits, copies=[torch.empty(n, dtype=BF16, device=dev)])
+        opt.load_state(m0, v0, 3)
+        return opt
+    want = p0.clone()
+    opt = make(want)
+    opt.step([g])
+    moments = [t.clone() for t in opt.state()]
+    del opt
+    sizes = sorted({n, n * 2, n * 4, n // 64})
+    torch.cuda.synchronize()
+    got, opt = p0.clone(), None
+    opt = make(got)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)                       # about 0.1 s
+    opt.step([g], stream=side)
+    state = opt.state(stream=side)
+    held = state if bits == 8 else None
+    del opt, state
+    used = [torch.full((s,), 0xFF, dtype=torch.uint8, device=dev) for s in sizes for _ in range(4)]
+    torch.cuda.synchronize()
+    del used
+    assert torch.equal(got, want)
+    if held is not None:
+        for a, b in zip(held, moments):
+            assert torch.equal(a, b)
+
+
 def test_operators_in_a_captured_graph(dev):
     gen = torch.Generator("cuda").manual_seed(17)
     counts, n, k = i32([100, 0, 44]), 128, 256
