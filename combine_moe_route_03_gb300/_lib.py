@@ -147,6 +147,7 @@ SIGNATURES = {
     "moe_adamw_decode": (_c_int, [_c_i64] + [_vp] * 7),
     "moe_adamw_encode": (_c_int, [_c_i64] + [_vp] * 7),
     "moe_read_status": (_c_int, [_vp, _vp]),
+    "moe_read_default_status": (_c_int, [_vp, _c_int]),
     "moe_last_cuda_error": (_c_int, []),
     "moe_num_sms": (_c_int, []),
     "moe_layer_forward": (_c_int, [ctypes.POINTER(Layer), _vp]),

@@ -21,7 +21,7 @@ __all__ = ["route", "eplb_build_map", "eplb_plan", "check_eplb_map", "EplbRecord
            "grouped_gemm_fp8", "combine", "read_status", "new_status", "MoELayer",
            "FMT_FP8", "FMT_BF16", "FMT_FP8_F32", "SCALE_UE8M0", "SCALE_F32", "GEMM_GATEUP_SWIGLU",
            "GEMM_DOWN", "num_sms", "scale_bytes", "weight_scales_f32",
-           "grouped_gemm", "grouped_wgrad", "swiglu", "swiglu_backward", "AdamW"]
+           "grouped_gemm", "grouped_wgrad", "swiglu", "swiglu_backward", "AdamW", "default_status"]
 
 
 def num_sms() -> int:
@@ -51,6 +51,16 @@ def new_status(device="cuda") -> torch.Tensor:
 def read_status(status: torch.Tensor) -> int:
     v = ctypes.c_int32(0)
     check(load().moe_read_status(ptr(status), ctypes.addressof(v)), "moe_read_status")
+    return int(v.value)
+
+
+def default_status(clear: bool = False) -> int:
+    """moe_read_default_status: the bits that grouped_gemm, grouped_wgrad, swiglu and
+    swiglu_backward calls without a status word have left on the current device; clear: and
+    zeroes them.  Wait for the calls' streams first."""
+    v = ctypes.c_int32(0)
+    check(load().moe_read_default_status(ctypes.addressof(v), int(clear)),
+          "moe_read_default_status")
     return int(v.value)
 
 
@@ -407,7 +417,8 @@ def grouped_gemm(x: torch.Tensor, w: torch.Tensor, counts: torch.Tensor, trans: 
     counts int32 [E]: rows of each expert; align / cap: where the segments start
     (align 128: a contiguous dispatch, 1: packed rows; cap: a masked dispatch).  Rows
     outside the segments are not written.  status: int32 word for what the device finds
-    wrong with the counts (new_status; without one it is not reported)."""
+    wrong with the counts, or a wait that gave up (new_status; default: the word that
+    default_status reads)."""
     if w.dim() != 3 or w.dtype not in _HALF:
         _expect(w, "w", _HALF, (None, None, None))
     E, n, k = w.shape

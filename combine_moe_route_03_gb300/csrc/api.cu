@@ -44,6 +44,16 @@ extern "C" int moe_read_status(const int32_t *status, int32_t *host_status) {
   return e == cudaSuccess ? MOE_OK : set_cuda_error(e);
 }
 
+extern "C" int moe_read_default_status(int32_t *host_status, int clear) {
+  if (!host_status) return MOE_ERR_INVALID;
+  int32_t a = 0, b = 0;
+  cudaError_t e = grouped_default_status(&a, clear != 0);
+  if (e == cudaSuccess) e = swiglu_default_status(&b, clear != 0);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  *host_status = a | b;
+  return MOE_OK;
+}
+
 // Redundant-expert placement: one replica for each of the N_phys - N_log most
 // loaded logical experts ("Large-scale EP ...", §EPLB: 256 logical experts in 288
 // physical slots, popular experts in several places, each copy taking a share).

@@ -14,6 +14,9 @@ namespace moe {
 
 // ------------------------------------------------------------------ host side
 int set_cuda_error(cudaError_t e);  // records e, returns MOE_ERR_CUDA
+// Bits that calls without a status word left in a source file's word (segments.cuh).
+cudaError_t grouped_default_status(int32_t *bits, bool clear);
+cudaError_t swiglu_default_status(int32_t *bits, bool clear);
 inline int check_launch() {
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? MOE_OK : set_cuda_error(e);

@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   auto fail = [&] {
     *abort = 1;
-    status_or(P.seg.status, MOE_STATUS_TIMEOUT);
+    segments_status(P.seg.status, MOE_STATUS_TIMEOUT);
   };
   // Waits for what takes a whole unit last longer the deeper the unit.
   const uint64_t unit_limit = kWaitLimitNs + 2000ull * ((kMode == kGrad ? P.seg.rows : P.nt) / BT);
@@ -1217,6 +1217,9 @@ int launch(const Maps &maps, const GroupedParams &P, int64_t max_units, int num_
 }
 
 }  // namespace
+
+cudaError_t grouped_default_status(int32_t *bits, bool clear) { return take_default_status(bits, clear); }
+
 }  // namespace moe
 
 using namespace moe;

@@ -8,6 +8,22 @@ namespace moe {
 
 constexpr int kMaxSegments = 1024;
 
+// What a call without a status word finds wrong goes into a word of the library: one for the
+// kernels of each source file, read by moe_read_default_status.
+namespace {
+__device__ int32_t default_status;
+}
+__device__ __forceinline__ void segments_status(int32_t *status, int bits) {
+  status_or(status ? status : &default_status, bits);
+}
+// Bits of this source file's word; `clear`: and zero in it.
+static inline cudaError_t take_default_status(int32_t *bits, bool clear) {
+  const cudaError_t e = cudaMemcpyFromSymbol(bits, default_status, sizeof *bits);
+  if (e != cudaSuccess || !clear || *bits == 0) return e;
+  const int32_t zero = 0;
+  return cudaMemcpyToSymbol(default_status, &zero, sizeof zero);
+}
+
 // Host-side check of a segment description (counts may be NULL where `all_rows`).
 inline int check_segments(const moe_segments &s, bool all_rows) {
   if (s.rows < 0) return MOE_ERR_INVALID;
@@ -124,7 +140,7 @@ __device__ void build_segments(const SegParams &P, SegTable &T, int *part, Weigh
     }
     __syncthreads();
   }
-  if (report && bad) status_or(P.status, bad);
+  if (report && bad) segments_status(P.status, bad);
 }
 
 // The segment that holds item i where each of the `before` sums counts `scale` items: the

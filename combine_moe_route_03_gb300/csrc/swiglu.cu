@@ -240,6 +240,9 @@ int swiglu(const moe_swiglu_args *a, bool backward, void *stream) {
 }
 
 }  // namespace
+
+cudaError_t swiglu_default_status(int32_t *bits, bool clear) { return take_default_status(bits, clear); }
+
 }  // namespace moe
 
 extern "C" int moe_swiglu(const moe_swiglu_args *args, void *stream) {

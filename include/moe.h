@@ -23,8 +23,8 @@
  *     MOE_ERR_CUDA: a CUDA launch or API error, the CUDA error is then available
  *     from moe_last_cuda_error()).
  *   - Errors found on the device are OR-ed into the caller's int32 `status` word
- *     (MOE_STATUS_* bits; sticky until the caller clears it).  moe_read_status()
- *     is the only call that waits for the device.
+ *     (MOE_STATUS_* bits; sticky until the caller clears it).  moe_read_status() and
+ *     moe_read_default_status() are the only calls that wait for the device.
  *   - Calls run on the calling thread's current CUDA device.  The first call on a
  *     device raises the kernels' shared-memory limits and caches cluster
  *     occupancy for that device (up to 64 devices per process).
@@ -475,7 +475,8 @@ int moe_combine(const moe_combine_cfg *cfg, const void *Y, const int32_t *row_of
  * What the device finds wrong is bounded, not followed: a negative count counts as 0 and
  * sets MOE_STATUS_BAD_INDEX; a segment that passes `rows` is cut there, and a count
  * above cap cut to it, and both set MOE_STATUS_CAPACITY.
- * The status words of these entry points are nullable.
+ * The status words of these entry points are nullable: without one the bits go into a
+ * word of the library, one a device (moe_read_default_status).
  * Limits: 1 <= E <= 1024, align >= 1, cap >= 0, 0 <= rows <= 2^31 - 1 - 1024.
  */
 typedef struct moe_segments {
@@ -629,6 +630,10 @@ int moe_adamw_encode(int64_t n, const float *m, const float *v, void *m_code, fl
 /* ------------------------------------------------------------------ status */
 /* Copies the device status word to *host_status (synchronous). */
 int moe_read_status(const int32_t *status, int32_t *host_status);
+/* The bits of all calls on the current device that had no status word of their own
+   (grouped products, gated activation) and have ended; clear != 0: and zeroes them.
+   Synchronous; does not wait for work on other streams.  Errors: NULL: MOE_ERR_INVALID. */
+int moe_read_default_status(int32_t *host_status, int clear);
 /* The last CUDA error an entry point saw (cudaError_t as int). */
 int moe_last_cuda_error(void);
 /* SM count of the current device. */

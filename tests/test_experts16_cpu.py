@@ -91,6 +91,10 @@ def test_grouped_wgrad_refusals(L):
         assert call(**kw) == UNSUPPORTED, kw
 
 
+def test_default_status_refusals(L):
+    assert L.moe_read_default_status(None, 0) == INVALID
+
+
 def test_swiglu_refusals(L):
     ok = dict(seg=seg(), I=16, type=0, gu=P16, out=P16)
     for name, more in (("moe_swiglu", {}), ("moe_swiglu_backward", dict(dh=P16, drow_w=P16))):

@@ -505,6 +505,37 @@ def test_swiglu_of_very_negative_gates(dev, I):
     assert not bool(h16.any())
 
 
+def test_errors_of_calls_without_a_status_word_are_kept(dev):
+    """Each operator, on the current and on another stream, and inside a graph; sticky until
+    cleared."""
+    gen = torch.Generator("cuda").manual_seed(27)
+    x, w = normal(gen, 12, 16), normal(gen, 2, 24, 16)
+    gu, dh, dy = normal(gen, 12, 32), normal(gen, 12, 16), normal(gen, 12, 24)
+    torch.cuda.synchronize()
+    api.default_status(clear=True)
+    side = torch.cuda.Stream()
+    for call in (lambda c, **kw: api.grouped_gemm(x, w, c, **kw),
+                 lambda c, **kw: api.grouped_wgrad(dy, x, c, **kw),
+                 lambda c, **kw: api.swiglu(gu, counts=c, **kw),
+                 lambda c, **kw: api.swiglu_backward(gu, dh, counts=c, **kw)):
+        for counts, bits in (([5, 7], 0), ([-1, 3], _lib.STATUS_BAD_INDEX), ([9, 9], _lib.STATUS_CAPACITY)):
+            for kw in ({}, dict(stream=side)):
+                call(i32(counts), **kw)
+                torch.cuda.synchronize()
+                assert api.default_status() == bits and api.default_status(clear=True) == bits
+                assert api.default_status() == 0
+        own = api.new_status()
+        call(i32([-1, 3]), status=own)
+        assert api.read_status(own) == _lib.STATUS_BAD_INDEX and api.default_status() == 0
+        c, g = i32([5, 7]), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            call(c)
+        c.copy_(i32([13, -9]))
+        g.replay()
+        torch.cuda.synchronize()
+        assert api.default_status(clear=True) == _lib.STATUS_CAPACITY | _lib.STATUS_BAD_INDEX
+
+
 def test_swiglu_gradient_is_the_difference_of_the_forward(dev):
     gen = torch.Generator("cuda").manual_seed(12)
     rows, I = 4, 16
