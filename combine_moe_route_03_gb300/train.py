@@ -22,7 +22,7 @@ import argparse
 
 import torch
 
-from . import api
+from . import _lib, api
 from .configs import CONTIG, SMALL_CONTIG, MoEConfig
 
 ALIGN = 128     # rows a contiguous dispatch rounds a segment up to
@@ -35,7 +35,8 @@ class ExpertTrainer:
 
     ``forward`` keeps what ``backward`` needs; ``backward`` returns the gradients of the
     input and of the routing weights, and adds to the weights' gradients (binary32) until
-    ``step`` applies and clears them, so several forward/backward pairs make one step."""
+    ``step`` applies and clears them, so several forward/backward pairs make one step.  What
+    the device finds wrong meanwhile is kept: ``check_status`` raises it."""
 
     def __init__(self, cfg: MoEConfig, W13: torch.Tensor, W2: torch.Tensor, state_bits: int = 32,
                  **adamw):
@@ -60,7 +61,7 @@ class ExpertTrainer:
     def forward(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor) -> torch.Tensor:
         """x bf16 [B][H], topk_idx and topk_w [B][K] (as api.route gives them) -> bf16 [B][H].
         A pair whose expert index lies outside [0, N) is left out, as dispatch and combine do:
-        it adds nothing, and the gradient of its weight is 0."""
+        it adds nothing, the gradient of its weight is 0, and check_status raises."""
         rows_x, d = self._dispatch(x, topk_idx)
         seg = dict(counts=d["counts"], align=ALIGN, status=self.status)
         row_of, rows = d["row_of"], d["rows"]
@@ -94,6 +95,17 @@ class ExpertTrainer:
         dx = api.grouped_gemm(dgu, self.W13, trans=True, **seg)
         return api.combine(dx, row_of, ones, status=self.status), drow_w[at].view(ones.shape)
 
+    def check_status(self) -> None:
+        """Raises if a call so far found something wrong on the device: pairs left out, a cut
+        segment, or a wait that gave up, whose results are incomplete.  Waits for the current
+        stream; call it as often as a result is relied on.  The word is cleared."""
+        torch.cuda.current_stream(self.status.device).synchronize()
+        bits = api.read_status(self.status)
+        if bits:
+            self.status.zero_()
+            names = [n for n in ("CAPACITY", "TIMEOUT", "BAD_INDEX") if bits & getattr(_lib, "STATUS_" + n)]
+            raise RuntimeError("device status " + (", ".join(names) or str(bits)))
+
     def step(self, grad_scale: torch.Tensor | None = None) -> None:
         """Applies the gradients added up since the last step."""
         if self._fresh:
@@ -126,8 +138,8 @@ def main(argv=None) -> list[float]:
         student.backward((diff * (2.0 / diff.shape[0])).to(torch.bfloat16))
         student.step()
         print(f"step {i}: loss {losses[-1]:.5f}")
-    if api.read_status(student.status):
-        raise RuntimeError("device status set")
+    teacher.check_status()
+    student.check_status()
     return losses
 
 

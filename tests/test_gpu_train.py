@@ -102,6 +102,21 @@ def test_micro_batches_add_up_and_a_step_clears_them(dev):
         assert torch.equal(g, h)                   # nothing of the last step is left in them
 
 
+def test_what_the_device_found_wrong_is_raised(dev):
+    W13, W2, x, dout, idx, w = make(SMALL, 3)
+    t = train.ExpertTrainer(SMALL, W13, W2)
+    t.forward(x, idx, w)
+    t.backward(dout)
+    t.check_status()
+    bad = idx.clone()
+    bad[0, 0] = -1
+    t.forward(x, bad, w)
+    t.backward(dout)
+    with pytest.raises(RuntimeError, match="BAD_INDEX"):
+        t.check_status()
+    t.check_status()
+
+
 @pytest.mark.parametrize("bits", ["8", "32"])
 def test_the_example_learns(dev, bits, capsys):
     losses = train.main(["--steps", "12", "--state-bits", bits])
