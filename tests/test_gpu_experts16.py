@@ -894,3 +894,31 @@ def test_wgrad_keeps_what_follows_a_segment_out(dev, n, k, align):
     for _ in range(10):
         assert torch.equal(api.grouped_wgrad(dy, x, c, align=align), want.to(BF16))
         assert torch.equal(api.grouped_wgrad(dy, x, c, align=align, out_dtype=F32), want)
+
+
+@pytest.mark.parametrize("n,k", [(1232, 672), (1096, 264), (264, 1032)])
+def test_wgrad_of_several_tiles_a_unit(dev, n, k):
+    """One pair, so that a unit takes several Q tiles over the P tiles that it holds: segments of
+    one block to six, longer ones in chunks with two accumulators, tails of every kind, a partial
+    last Q tile.  Whole numbers: equality."""
+    gen = torch.Generator("cuda").manual_seed(28)
+    for counts, align in (([65, 319, 320, 321, 384, 385, 449, 513, 769, 1300], 1),
+                          ([1300, 1, 0, 383, 400, 64, 63, 7, 777, 128, 129, 192, 255, 256, 0, 5000], 64),
+                          ([16, 15, 17, 48, 31, 33, 97, 80, 200, 79, 1, 2, 3, 4, 5, 6], 64)):
+        rows, starts = rows_of(counts, align), starts_of(counts, align)
+        dy = torch.full((rows, n), float("nan"), dtype=BF16, device=dev)
+        x = torch.full((rows, k), float("nan"), dtype=BF16, device=dev)
+        want = torch.zeros(len(counts), n, k, device=dev)
+        for e, (m, s) in enumerate(zip(counts, starts)):
+            dy[s:s + m] = torch.randint(-3, 4, (m, n), generator=gen, device=dev).to(BF16)
+            x[s:s + m] = torch.randint(-3, 4, (m, k), generator=gen, device=dev).to(BF16)
+            want[e] = (dy[s:s + m].double().t() @ x[s:s + m].double()).float()
+        tiles = len(counts) * -(-k // 256) * -(-n // 256)
+        for sms in (2, 4, 0):
+            assert sms == 0 or tiles // (16 * (sms // 2)) >= (2 if sms == 2 else 1)
+            for dtype in (BF16, F16):
+                out = torch.full((len(counts), n, k), -7.0, dtype=dtype, device=dev)
+                for _ in range(3):
+                    got = api.grouped_wgrad(dy.to(dtype), x.to(dtype), i32(counts), align=align, out=out, num_sms_=sms)
+                    assert torch.equal(got, want.to(dtype))
+            assert torch.equal(api.grouped_wgrad(dy, x, i32(counts), align=align, out_dtype=F32, num_sms_=sms), want)
