@@ -718,7 +718,8 @@ class MoELayer:
         self.A_sf = t(scale_bytes(rows, H, afmt))
         self.H1 = t(rows, I)
         self.H1_sf = t(scale_bytes(rows, I, afmt))
-        # rows without a token are never written: they hold zeros, not what was in memory
+        # A call writes the rows of its tokens alone: the others hold zeros until a token
+        # first lands there, then what the last call that filled the row left.
         self.Y = t(rows, H, dtype=torch.bfloat16).zero_()
         self.S = self.Y[self.rows:] if cfg.shared else None
         self.signal = t(rows // cfg.block_m_signal, dtype=torch.int32) if cfg.sbo else None
