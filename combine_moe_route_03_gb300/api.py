@@ -392,6 +392,18 @@ def _is(t, what: str, dtype: torch.dtype, shape: tuple) -> None:
         _expect(t, what, (dtype,), shape)
 
 
+def _is_half(t, what: str, dims: int) -> None:
+    if not (isinstance(t, torch.Tensor) and t.dtype in _HALF and t.dim() == dims):
+        _expect(t, what, _HALF, (None,) * dims)
+
+
+def _is_status(status) -> None:
+    """The kernels OR 32 bits into it."""
+    if status is not None and not (isinstance(status, torch.Tensor) and status.dtype == torch.int32
+                                   and status.numel() > 0):
+        _expect(status, "status", (torch.int32,), (1,))
+
+
 def _is_counts(counts) -> None:
     if not (isinstance(counts, torch.Tensor) and counts.dtype == torch.int32 and counts.dim() == 1):
         _expect(counts, "counts", (torch.int32,), (None,))
@@ -419,12 +431,13 @@ def grouped_gemm(x: torch.Tensor, w: torch.Tensor, counts: torch.Tensor, trans: 
     outside the segments are not written.  status: int32 word for what the device finds
     wrong with the counts, or a wait that gave up (new_status; default: the word that
     default_status reads)."""
-    if w.dim() != 3 or w.dtype not in _HALF:
-        _expect(w, "w", _HALF, (None, None, None))
+    _is_half(w, "w", 3)
+    _is_half(x, "x", 2)
     E, n, k = w.shape
     red, cols = (n, k) if trans else (k, n)
     rows = x.shape[0]
     _is(x, "x", w.dtype, (rows, red))
+    _is_status(status)
     _is(counts, "counts", torch.int32, (E,))
     if out is None:
         out = torch.empty((rows, cols), dtype=w.dtype, device=x.device)
@@ -447,6 +460,7 @@ def grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, counts: torch.Tensor, align
     grouped_gemm's weights, in dy's type or (out_dtype torch.float32) in binary32.
     accumulate: add to ``out`` (binary32) instead of overwriting it."""
     _expect(dy, "dy", _HALF, (None, None))
+    _is_status(status)
     rows, n = dy.shape
     _expect(x, "x", (dy.dtype,), (rows, None))
     k = x.shape[1]
@@ -474,8 +488,8 @@ def swiglu(gu: torch.Tensor, row_w: torch.Tensor | None = None,
     """moe_swiglu: gu bf16 / fp16 [rows][2I] (gate, then up columns) -> w silu(g) u
     [rows][I]; row_w fp32 [rows] (default 1).  counts / align / cap / status: only the
     rows of these segments (see grouped_gemm); default all rows."""
-    if gu.dim() != 2 or gu.dtype not in _HALF:
-        _expect(gu, "gu", _HALF, (None, None))
+    _is_half(gu, "gu", 2)
+    _is_status(status)
     rows, I2 = gu.shape
     if I2 % 2:
         raise ValueError("gu: an even number of columns expected")
@@ -501,8 +515,8 @@ def swiglu_backward(gu: torch.Tensor, dh: torch.Tensor, row_w: torch.Tensor | No
                     status: torch.Tensor | None = None, stream=None):
     """moe_swiglu_backward: dh [rows][I], the gradient of swiglu's output -> (dgu
     [rows][2I], drow_w fp32 [rows], or None without row_w).  dgu may be gu itself."""
-    if gu.dim() != 2 or gu.dtype not in _HALF:
-        _expect(gu, "gu", _HALF, (None, None))
+    _is_half(gu, "gu", 2)
+    _is_status(status)
     rows, I2 = gu.shape
     if I2 % 2:
         raise ValueError("gu: an even number of columns expected")

@@ -222,3 +222,26 @@ def test_adamw_refuses_gradients_that_are_no_tensors(calls):
         with pytest.raises(TypeError, match="torch tensor"):
             opt.step([torch.zeros(4), bad])
     assert calls.names == [] and opt.steps == 0
+
+
+def test_binding_refuses_what_is_no_tensor_and_other_status_words(calls):
+    """Neither ends in an attribute error or reaches the library: the kernels write 32 bits."""
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    c4, w = torch.zeros(4, dtype=torch.int32), bf(4, 16, 24)
+    for call in (lambda: api.grouped_gemm(None, w, c4), lambda: api.grouped_gemm(bf(8, 24), None, c4),
+                 lambda: api.grouped_gemm(bf(8, 24), w, None), lambda: api.grouped_wgrad(None, bf(8, 24), c4),
+                 lambda: api.grouped_wgrad(bf(8, 16), None, c4), lambda: api.swiglu(None),
+                 lambda: api.swiglu_backward(None, bf(8, 16)), lambda: api.swiglu_backward(bf(8, 32), None)):
+        with pytest.raises(TypeError, match="torch tensor"):
+            call()
+    for status in (torch.zeros(1, dtype=torch.uint8), torch.zeros(1, dtype=torch.int16), torch.zeros(1),
+                   torch.zeros(0, dtype=torch.int32)):
+        for call in (lambda: api.grouped_gemm(bf(8, 24), w, c4, status=status),
+                     lambda: api.grouped_wgrad(bf(8, 16), bf(8, 24), c4, status=status),
+                     lambda: api.swiglu(bf(8, 32), counts=c4, status=status),
+                     lambda: api.swiglu_backward(bf(8, 32), bf(8, 16), counts=c4, status=status)):
+            with pytest.raises(ValueError, match="status"):
+                call()
+    assert calls.names == []
+    api.grouped_gemm(bf(8, 24), w, c4, status=torch.zeros((), dtype=torch.int32))
+    assert calls.names == ["moe_grouped_gemm"]
