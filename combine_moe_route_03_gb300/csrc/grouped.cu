@@ -76,7 +76,7 @@ constexpr uint32_t kPBytes = 128 * BT * 2;  // a CTA's half of a P tile
 // 32 16-bit values, or three in turn of 16 x 32 binary32 ones.
 constexpr uint32_t kStage = 2048;
 constexpr int kStages = 3;  // (two and six P slots: 464 against 434 us, 16 x ~512 rows)
-constexpr uint32_t ring_bytes(int mode, bool f32) { return (mode != kGrad ? 212 : f32 ? 164 : 196) * 1024; }
+constexpr uint32_t ring_bytes(int mode, bool f32) { return (mode != kGrad ? 212 : f32 ? 160 : 192) * 1024; }
 constexpr uint32_t stage_bytes(int mode, bool f32) { return mode != kGrad ? 0 : f32 ? kStages * kStage : kStage; }
 constexpr int kSumBlocks = 8;    // blocks of one partial sum (binary32 output): 512 rows
 constexpr int kJoinBlocks = 64;  // of a joined sum with 16-bit output
