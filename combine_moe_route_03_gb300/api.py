@@ -593,35 +593,39 @@ class AdamW:
                 t.m, t.v = ptr(self.m_code) + o, ptr(self.r_code) + o
                 t.m_scale = ptr(self.m_scale) + o // self.BLOCK * 4
                 t.r_scale = ptr(self.r_scale) + o // self.BLOCK * 4
-        self._places = [self._place(t) for t in self._held()]
+        # what a step compares, as cheaply as it can (20 tensors and copies: 8 us of a step's 30)
+        self._places = [(p.data_ptr(), p.shape, *((None, None) if c is None else
+                                                  (c.data_ptr(), c.dtype)))
+                        for p, c in zip(self.params, self.copies)]
+        self._moment_places = [t.data_ptr() for t in self._moments()]
+
+    def _moments(self) -> tuple:
+        return ((self.m, self.v) if self.state_bits == 32 else
+                (self.m_code, self.r_code, self.m_scale, self.r_scale))
 
     def _held(self) -> list:
         """Every tensor whose address the table holds."""
-        moments = ((self.m, self.v) if self.state_bits == 32 else
-                   (self.m_code, self.r_code, self.m_scale, self.r_scale))
-        return [*self.params, *(c for c in self.copies if c is not None), *moments]
-
-    @staticmethod
-    def _place(t: torch.Tensor) -> tuple:
-        return t.data_ptr(), t.numel(), t.dtype, t.is_contiguous()
+        return [*self.params, *(c for c in self.copies if c is not None), *self._moments()]
 
     def step(self, grads, grad_scale: torch.Tensor | None = None, stream=None) -> None:
         """One step with one gradient (bf16, fp16 or fp32, the parameter's shape) per
         parameter; grad_scale: fp32 device scalar that multiplies every gradient."""
         if len(grads) != len(self.params):
             raise ValueError(f"{len(self.params)} gradients expected, got {len(grads)}")
-        place, held = self._place, self._held()
-        if [place(t) for t in held] != self._places:
-            raise ValueError("the storage, size and type that parameters, copies and moments had "
-                             "when this AdamW was made expected")
         for g in grads:
             if not isinstance(g, torch.Tensor):
                 raise TypeError("gradient: a torch tensor is required (one for each parameter)")
         addresses, s = ptrs(*grads)
-        for t, p, g, a in zip(self._table, self.params, grads, addresses):
+        same = [t.data_ptr() for t in self._moments()] == self._moment_places
+        for t, p, c, (at, shape, c_at, c_type), g, a in zip(self._table, self.params, self.copies,
+                                                            self._places, grads, addresses):
+            if (not same or p.data_ptr() != at or p.shape != shape or not p.is_contiguous()
+                    or (c is not None and (c.data_ptr() != c_at or c.dtype != c_type))):
+                raise ValueError("the storage, size and type that parameters, copies and moments "
+                                 "had when this AdamW was made expected")
             kind = _TYPES.get(g.dtype)
-            if kind is None or g.shape != p.shape:
-                raise ValueError(f"gradient: {tuple(p.shape)} of dtype bf16, fp16 or fp32 "
+            if kind is None or g.shape != shape:
+                raise ValueError(f"gradient: {tuple(shape)} of dtype bf16, fp16 or fp32 "
                                  f"expected, got {tuple(g.shape)} {g.dtype}")
             t.g, t.g_type = a, kind
         if grad_scale is not None:
@@ -630,8 +634,9 @@ class AdamW:
                 raise ValueError("grad_scale: one value expected")
         cfg = AdamwCfg(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
                        self.steps + 1, self.state_bits, ptr(grad_scale))
-        check(load().moe_adamw(ctypes.byref(cfg), self._table, len(self.params),
-                               _on(stream, s, *grads, grad_scale, *held)), "moe_adamw")
+        if stream is not None:
+            s = _ordered(stream, *grads, grad_scale, *self._held())
+        check(load().moe_adamw(ctypes.byref(cfg), self._table, len(self.params), s), "moe_adamw")
         self.steps += 1
 
     def state(self, stream=None):
