@@ -255,12 +255,13 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
                "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
 }
-// Arrive on an mbarrier of either CTA of the pair where only the count matters (operands
-// land by TMA, accumulators are read by tcgen05.ld): no cluster-wide release, which would
-// first wait for the warp's global stores.  What orders this CTA's own writes before the
-// other CTA's reads takes mbar_arrive_pair.
+// Arrive on an mbarrier of either CTA of the pair where no writes of this CTA's threads have
+// to be ordered: operands land by TMA, and reads of an accumulator are ordered by the tcgen05
+// fences before the arrival and after the (cluster-wide, relaxed) wait.  A release would first
+// wait for the warp's global stores.  Writes take mbar_arrive_pair.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
 }
 // Where the pair's MMAs read what threads of the other CTA wrote to its shared memory: an
 // arrival that releases those writes (the thread's, and those it has synchronised with) at
@@ -284,12 +285,18 @@ __device__ __forceinline__ bool mbar_try_wait_relaxed(uint32_t bar, uint32_t par
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool mbar_wait_pair(uint32_t bar, uint32_t parity, volatile int *abort,
-                                               uint64_t limit_ns) {
+__device__ __forceinline__ bool mbar_wait_relaxed(uint32_t bar, uint32_t parity, volatile int *abort,
+                                                  uint64_t limit_ns) {
+  if (mbar_try_wait_relaxed(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
 #pragma unroll 1
   while (!mbar_try_wait_relaxed(bar, parity))
     if (*abort || globaltimer() - t0 > limit_ns) return false;
+  return true;
+}
+__device__ __forceinline__ bool mbar_wait_pair(uint32_t bar, uint32_t parity, volatile int *abort,
+                                               uint64_t limit_ns) {
+  if (!mbar_wait_relaxed(bar, parity, abort, limit_ns)) return false;
   asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
   return true;
 }
@@ -730,6 +737,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 ((uint32_t)(BP >> 4) << 24);
         int acc = 0;
         bool ok = true;
+        // accumulator number a has been read: the one before it in the same place (flip), or itself
+        auto wait_acc = [&](int a, uint32_t flip) {
+          const bool read = mbar_wait_relaxed(bar_acc_empty + 8 * (a & 1), ((uint32_t)(a >> 1) & 1u) ^ flip,
+                                              abort, kWaitLimitNs);
+          if (!read) fail();
+          return read;
+        };
         // 64-deep blocks, the last one in steps of 16; the accumulator d starts anew at the first
         auto multiply = [&](uint32_t d, uint64_t dp, uint64_t dq, uint32_t idesc, int steps, bool more) {
           mma_pair_f16(d, dp, dq, idesc, more);
@@ -759,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int a = join ? acc : acc + g;
                 const bool fresh = join || b0 == 0;
                 if (fresh) {
-                  ok = wait(bar_acc_empty + 8 * (a & 1), ((uint32_t)(a >> 1) & 1u) ^ 1u, kWaitLimitNs);
+                  ok = wait_acc(a, 1u);
                   if (!ok) break;
                   tc_fence_after();
                 }
@@ -810,8 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int b0 = 0; ok && b0 < U.blocks; b0 += piece) {
               const int b1 = min(U.blocks, b0 + piece);
               for (int a = 0; a < accs && ok; ++a)
-                ok = wait(bar_acc_empty + 8 * ((acc + a) & 1), ((uint32_t)((acc + a) >> 1) & 1u) ^ 1u,
-                          kWaitLimitNs);
+                ok = wait_acc(acc + a, 1u);
               if (!ok) break;
               tc_fence_after();
               for (int b = b0; b < b1; ++b) {
@@ -836,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // so do the odd CTA's last releases
         if (rank == 0)
           for (int a = max(0, acc - 2); ok && a < acc; ++a)
-            ok = wait(bar_acc_empty + 8 * (a & 1), (uint32_t)(a >> 1) & 1u, kWaitLimitNs);
+            ok = wait_acc(a, 0u);
       }
     } else if (warp == 2 && lane == 0) {
       // --------------------------------------------------------- scheduler
