@@ -130,3 +130,24 @@ def test_refuses_other_layouts(dev):
             train.ExpertTrainer(cfg, W13, W2)
     with pytest.raises(ValueError, match="expected"):
         train.ExpertTrainer(SMALL, W2, W13)
+
+
+def test_masked_rows_through_the_chain(dev):
+    """The decode layout: dispatch into slots of `cap` rows, both products and the activation over
+    them, combine; against the layer's definition.  Slots past a count hold NaN."""
+    cfg = SMALL.with_(layout=configs.MASKED, cap=128)
+    W13, W2, x, dout, idx, w = make(cfg, 4)
+    status = api.new_status()
+    d = api.dispatch(cfg, x, idx, fmt=api.FMT_BF16, status=status)
+    rows_x, row_of = d["A"].view(torch.bfloat16), d["row_of"]
+    live = torch.zeros(d["rows"], dtype=torch.bool, device=dev)
+    live[row_of.long().reshape(-1)] = True
+    rows_x[~live] = float("nan")
+    row_w = torch.full((d["rows"],), float("nan"), device=dev)
+    row_w[row_of.long().reshape(-1)] = w.reshape(-1)
+    seg = dict(counts=d["counts"], cap=cfg.cap, status=status)
+    gu = api.grouped_gemm(rows_x, W13.bfloat16(), **seg)
+    y = api.grouped_gemm(api.swiglu(gu, row_w=row_w, **seg), W2.bfloat16(), **seg)
+    out = api.combine(y, row_of, torch.ones_like(w), status=status)
+    assert api.read_status(status) == 0
+    assert off(out, reference(cfg, W13, W2, x, dout, idx, w)[0]) <= OUT
