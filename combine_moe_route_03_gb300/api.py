@@ -2,6 +2,11 @@
 
 Only marshalling happens here (shape checks, output allocation through torch,
 pointer passing); each step of the layer runs in the library's CUDA kernels.
+
+None of the calls takes part in automatic differentiation: results carry no graph whatever
+their inputs require, and what is written in place (``out=``, ``dgu=gu``, the parameters,
+copies and moments of ``AdamW``) does not raise the tensors' version counters.  Gradients
+are the caller's to chain, as ``train.ExpertTrainer`` does.
 """
 from __future__ import annotations
 

@@ -8,7 +8,7 @@
 // table travels as a kernel parameter: nothing is kept on the device between calls.
 // Bound by memory with binary32 moments: 28 bytes a value with 16-bit gradients and a 16-bit
 // copy, 7.0 TB/s over 201 M values (803 us).  With 8-bit moments 16 bytes a value and 97
-// instructions: 6.1 TB/s (526 us), about 80 % of the issue slots.
+// instructions: 6.1 TB/s (526 us), 85 % of the issue slots.
 #include <cuda_fp16.h>
 #include <math.h>
 #include <string.h>

@@ -50,7 +50,7 @@
 //     in each SM; 64 KB gave 4.6 TB/s.
 //   about 256 rows, ragged: weights, rows and output from and to HBM, 676 us (6.1 TB/s).
 //   many rows: the tensor cores under the power cap, 1560 to 1960 TFLOP/s.
-//   gradient, 16 experts of about 256 rows: 191 us, 4.9 TB/s of writes, shared memory 77 %
+//   gradient, 16 experts of about 256 rows: 194 us, 4.8 TB/s of writes, shared memory 77 %
 //     busy (copies in, MMAs, staging); zeros alone are written at 6.9 TB/s, the MMAs alone
 //     would take 110 us.  2048 rows: 961 us, 2000 TFLOP/s.
 // Tried and not kept: requests into L2 ahead of the ring (560 -> 667 us, they queue before

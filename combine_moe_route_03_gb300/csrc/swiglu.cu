@@ -190,9 +190,9 @@ int launch(const SwigluParams &P, bool vec, cudaStream_t st) {
   const int groups = wide ? 1 : kThreads / 32;
   const int64_t need = ((int64_t)P.seg.rows + groups - 1) / groups;
   // Eight blocks an SM are resident.  The forward over long rows gains from three times as
-  // many blocks, handed out as others end (I = 2048: 134 us against 142); each block builds
-  // the segments' table, which short rows (I = 520: 47.5 against 45.7) and the backward's
-  // longer ones (217.7 against 213.1) do not repay.
+  // many blocks, handed out as others end (I = 2048: 131 us against 146; I = 520: 45 and
+  // 46, left alone); each block builds the segments' table, which the backward does not repay
+  // (I = 2048: 215 us against 211; 520: 78 against 75).
   const int64_t most = (int64_t)device_sm_count() * (!kBackward && P.I >= 1024 ? 24 : 8);
   const unsigned grid = (unsigned)(need < most ? need : most);
   if (vec) {

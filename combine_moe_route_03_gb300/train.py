@@ -10,7 +10,8 @@ then carries through: the combine only sums a token's rows.  So the backward nee
 permutation of its own: the rows' gradient is the dispatch of the output's gradient, and
 the input's gradient the combine of the rows' (both with unit weights).  The gradients of
 the routing weights come out of the activation's backward; the router itself (its choice of
-experts and its weights) is the caller's to train.
+experts and its weights) is the caller's to train.  A shared expert of the configuration is
+no part of this: outputs and gradients are the routed experts' alone.
 
     python -m combine_moe_route_03_gb300.train [--steps N] [--state-bits 8|32]
 
