@@ -109,6 +109,13 @@ __device__ __forceinline__ float of_key(uint32_t k) {
 __device__ __forceinline__ float quick_sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(fminf(-z, 87.0f))); }
 // Two choice scores that binary32 tells apart wrongly lie closer than this.
 __device__ __forceinline__ float margin(float c) { return 0x1p-19f * fmaxf(1.0f, fabsf(c)); }
+// How far a + b, the sum of a group's two best scores, may be off: by the errors of both (each a
+// sigmoid's 2^-21 and a rounding, half its margin at most) and its own rounding.  The sum itself
+// says nothing of that: of scores of either sign it may be next to 0 where they are large.
+__device__ __forceinline__ float group_error(float a, float b) {
+  const float sum = a + b;
+  return sum > -INFINITY ? 0.5f * (margin(a) + margin(b)) : 0.0f;
+}
 
 __device__ __forceinline__ double sigmoid64(float z) {
   const double x = exp(-fabs((double)z));
@@ -271,21 +278,22 @@ __device__ __forceinline__ int choose(const RouteParams &P, int64_t t, const flo
       a = fmaxf(a, oa);
     }
     const float s = a + b;
-    const float err = P.sigmoid ? 0.0f : sum_error(a, b, s);
+    const float low_bits = P.sigmoid ? 0.0f : sum_error(a, b, s);
     int ahead = 0;
     for (int j = 0; j < P.n_group; ++j) {
-      const float os = __shfl_sync(kAll, s, j * share), oe = __shfl_sync(kAll, err, j * share);
-      ahead += os > s || (os == s && (oe > err || (oe == err && j < g)));
+      const float os = __shfl_sync(kAll, s, j * share), oe = __shfl_sync(kAll, low_bits, j * share);
+      ahead += os > s || (os == s && (oe > low_bits || (oe == low_bits && j < g)));
     }
     bool kept = g < P.n_group && ahead < P.topk_group;
     if (P.sigmoid && P.topk_group < P.n_group) {
-      // the kept group that is nearest to the border, and the nearest one left out
-      const uint32_t in = __reduce_min_sync(kAll, kept ? key_of(s) : kAll);
-      const uint32_t out = __reduce_max_sync(kAll, g < P.n_group && !kept ? key_of(s) : 0u);
-      const float low = of_key(in), high = of_key(out), near = 2.0f * margin(low);
-      if (in != 0 && out != 0 && low - high <= near) {
+      // the least that a kept group may have, and the most that one left out may
+      const float err = group_error(a, b);
+      const uint32_t in = __reduce_min_sync(kAll, kept ? key_of(s - err) : kAll);
+      const uint32_t out = __reduce_max_sync(kAll, g < P.n_group && !kept ? key_of(s + err) : 0u);
+      const float low = of_key(in), high = of_key(out);
+      if (in != 0 && out != 0 && low <= high) {
         // groups on either side that may belong to the other, by the sums of their best in 64 bits
-        const bool open = g < P.n_group && (kept ? s <= high + near : s >= low - near);
+        const bool open = g < P.n_group && (kept ? s - err <= high : s + err >= low);
         const uint32_t open_lanes = __ballot_sync(kAll, open);
         uint32_t marks = 0;
 #pragma unroll
@@ -692,8 +700,7 @@ __global__ void __launch_bounds__(kQuadWarps * 32, 3) route_topk_quad_kernel(con
               b = b == -INFINITY ? b : quick_sigmoid(b);
             }
             const float s = a + b;
-            if (q == 0) sum[g] = s;
-            if (!P.sigmoid && q == 0) err[g] = sum_error(a, b, s);
+            if (q == 0) sum[g] = s, err[g] = P.sigmoid ? group_error(a, b) : sum_error(a, b, s);
             a = b = -INFINITY;
             in_group = 0;
             ++g;
@@ -702,7 +709,8 @@ __global__ void __launch_bounds__(kQuadWarps * 32, 3) route_topk_quad_kernel(con
         __syncwarp();
         // kept: fewer than topk_group groups rank before it; four lanes, a group each in turn
         uint32_t kept;
-        float lowest, highest, least;  // of the kept, of the others; second best of a kept group
+        // the least that a kept group may have, the most of the others; least second best of the kept
+        float lowest, highest, least;
         auto rank = [&](auto before) {  // before(j, g): group j ranks before group g
           kept = 0;
           lowest = least = INFINITY;
@@ -715,10 +723,10 @@ __global__ void __launch_bounds__(kQuadWarps * 32, 3) route_topk_quad_kernel(con
             for (int j = 0; j < P.n_group; ++j) ahead += before(j, g);
             if (ahead < P.topk_group) {
               kept |= 1u << g;
-              lowest = fminf(lowest, sum[g]);
+              lowest = fminf(lowest, sum[g] - err[g]);
               least = fminf(least, seconds[i]);
             } else {
-              highest = fmaxf(highest, sum[g]);
+              highest = fmaxf(highest, sum[g] + err[g]);
             }
           }
 #pragma unroll
@@ -735,11 +743,10 @@ __global__ void __launch_bounds__(kQuadWarps * 32, 3) route_topk_quad_kernel(con
           rank([&](int j, int g) {
             return sum[j] > sum[g] || (sum[j] == sum[g] && (err[j] > err[g] || (err[j] == err[g] && j < g)));
           });
-        const bool border = P.sigmoid && lowest > -INFINITY && highest > -INFINITY && lowest - highest <= 2.0f * margin(lowest);
+        const bool border = P.sigmoid && lowest > -INFINITY && highest > -INFINITY && lowest <= highest;
         if (__any_sync(kAll, border)) {
           // The sums of the groups at the border in 64 bits, of the others as they are, where the
           // binary32 ones were.
-          const float near = 2.0f * margin(lowest);
           double exact[kMostGroups / 4], *sums = reinterpret_cast<double *>(sum);
 #pragma unroll
           for (int i = 0; i < kMostGroups / 4; ++i) {
@@ -747,7 +754,7 @@ __global__ void __launch_bounds__(kQuadWarps * 32, 3) route_topk_quad_kernel(con
             if (g >= P.n_group) break;
             const float s = sum[g];
             exact[i] = (double)s;
-            if (!border || s < lowest - near || s > highest + near) continue;
+            if (!border || s + err[g] < lowest || s - err[g] > highest) continue;
             const float from = seconds[i] - margin(seconds[i]);
             const float *all = values - q * 8 + g * per_group * 32;
             double best = -INFINITY, next = -INFINITY;

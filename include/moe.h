@@ -695,8 +695,9 @@ int moe_rms_norm_backward(const moe_norm_grad_args *args, void *workspace, size_
  * moe_route's choice and weights from given logits [B][N] of `type` (MOE_TYPE_*); cfg->H is
  * not used.  What differs from moe_route:
  *   - the choice is that of the real numbers z, sigmoid(z) + bias: where binary32 cannot tell
- *     two scores apart that matter they are compared in binary64; without a bias experts are
- *     compared by their logits (sums of two past binary32's range: by their first 24 bits).
+ *     two scores apart that matter, or two groups' sums, they are compared in binary64; without
+ *     a bias experts are compared by their logits (sums of two past binary32's range: by their
+ *     first 24 bits).
  *     Equal scores: the lower index.
  *   - a logit of -inf or NaN masks its expert (as a bias of -inf or NaN does): it is never
  *     chosen and weighs nothing.  A group with fewer than two experts left scores -inf.  Where

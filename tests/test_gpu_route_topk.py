@@ -376,3 +376,40 @@ def test_groups_a_few_last_bits_of_64_apart(dev, B):
     z[:, 3], z[:, 40] = 34.0, 36.0
     z[:, 9] = z[:, 33] = torch.randn(B, generator=torch.Generator("cuda").manual_seed(3), device=dev)
     assert api.route_topk(cfg, z)["topk_idx"].unique(dim=0).tolist() == [[40, 33]]
+
+
+@pytest.mark.parametrize("B", [64, 8200])
+@pytest.mark.parametrize("most", [1e2, 1e4, 1e5, 1e7])
+def test_groups_whose_two_best_scores_cancel(dev, most, B):
+    """One expert of each group lifted as far as the others are lowered: the sum of a group's two
+    best scores is near 1, but carries the rounding of numbers as large as the biases."""
+    gen = torch.Generator("cuda").manual_seed(int(most))
+    for K, topk in ((8, 4), (2, 1), (5, 7)):
+        cfg = config(B, N=256, K=K, n_group=8, topk_group=topk, score_fn=SIG, renorm=1)
+        bias = torch.full((8, 32), -most, device=dev)
+        bias.scatter_(1, torch.randint(32, (8, 1), generator=gen, device=dev), most)
+        z = torch.randn(B, 256, generator=gen, device=dev) * 0.02          # sums within 0.04 of one another
+        z[1::2] *= 50
+        pick = torch.arange(0, B, max(1, B // 64), device=dev)
+        for zs in (z, z.to(BF16)):
+            got = api.route_topk(cfg, zs, bias.view(-1))["topk_idx"]
+            assert torch.equal(got[pick], choose(cfg, zs[pick], bias.view(-1)))
+
+
+@pytest.mark.parametrize("B", [64, 8200])
+def test_groups_with_biases_of_every_size(dev, B):
+    """Some groups with large scores of both signs beside others with small ones: how far apart
+    binary32 can tell two sums depends on the groups compared."""
+    gen = torch.Generator("cuda").manual_seed(31)
+    for size in (8, 32):
+        cfg = config(B, N=8 * size, K=4, n_group=8, topk_group=3, score_fn=SIG, renorm=1)
+        for _ in range(6):
+            bias = torch.randn(8, size, generator=gen, device=dev) * 0.01
+            most = 10.0 ** (torch.rand(8, generator=gen, device=dev) * 7)
+            wide = torch.rand(8, generator=gen, device=dev) < 0.5
+            bias[wide] -= most[wide, None]
+            bias[wide, 3] += 2 * most[wide]                               # near 1 again, with one of -most
+            z = torch.randn(B, 8 * size, generator=gen, device=dev) * 0.02
+            pick = torch.arange(0, B, max(1, B // 64), device=dev)
+            got = api.route_topk(cfg, z, bias.view(-1))["topk_idx"]
+            assert torch.equal(got[pick], choose(cfg, z[pick], bias.view(-1)))
