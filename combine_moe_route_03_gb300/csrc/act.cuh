@@ -6,20 +6,30 @@
 namespace moe {
 namespace {
 
-// The normal distribution function, and e^(-z^2 / 2) that it needs on the way: erfc by
-// Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26, within 1.5e-7 (half of it
-// here).  Its tail on the left is a product, so nothing cancels there.  The library's erff takes
-// twice the instructions, along two branches of which a warp mostly runs both (slopes of 8192 x
-// 4096 values: 52 us, 44 so).
+// The normal distribution function, and e^(-z^2 / 2) that it needs on the way.  For x >= 0
+//   Phi(-x) = e^(-x^2 / 2) t P(t),  t = 1 / (1 + 0.4 x),
+// with P of degree 9 fitted for x up to 13.5 by weighted least squares whose weights rise where the
+// relative error is large (Lawson's iteration), to 2^-26 of the value; on the right 1 - Phi(-z).
+// The tail on the left is a product, so it keeps its relative error where the function is next to
+// nothing: with the quotient and the exponential within 2^-22 of theirs, all of it is within
+// 1.15 2^-20 (1 + z^2 / 8) of the value (the second term: the exponential's argument in binary32).
+// (Slopes of 8192 x 4096 values: 46 us, of silu 44.  Abramowitz and Stegun 7.1.26, four
+// multiplications fewer, took 45, but its absolute error passes a 16-bit rounding of the value
+// left of z = -3.6; the library's erff takes two branches, of which a warp mostly runs both: 52.)
 __device__ __forceinline__ float normal_cdf(float z, float &e) {
-  const float x = fabsf(z) * 0.70710678118654752f, t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
-  float p = 1.061405429f;
-  p = fmaf(p, t, -1.453152027f);
-  p = fmaf(p, t, 1.421413741f);
-  p = fmaf(p, t, -0.284496736f);
-  p = fmaf(p, t, 0.254829592f);
-  e = __expf(-x * x);
-  const float q = 0.5f * p * t * e;
+  const float x = fabsf(z), t = __fdividef(1.0f, fmaf(0.4f, x, 1.0f));
+  float p = 0.0319654532f;
+  p = fmaf(p, t, -0.175461844f);
+  p = fmaf(p, t, 0.379125178f);
+  p = fmaf(p, t, -0.36978963f);
+  p = fmaf(p, t, 0.115964055f);
+  p = fmaf(p, t, -0.0249578636f);
+  p = fmaf(p, t, 0.090691641f);
+  p = fmaf(p, t, 0.133274511f);
+  p = fmaf(p, t, 0.159611866f);
+  p = fmaf(p, t, 0.159576654f);
+  e = __expf(-0.5f * x * x);
+  const float q = p * t * e;
   return z < 0.0f ? q : 1.0f - q;
 }
 

@@ -733,7 +733,8 @@ int moe_route_topk_backward(const moe_route_cfg *cfg, int type, const void *logi
  *   out = act(z) + residual, w [n][k],
  * for out_type `type` or MOE_TYPE_F32, one rounding at the end.  bias float (nullable);
  * residual (nullable) of out_type and out's shape, may be out itself; act MOE_ACT_*: relu,
- * gelu (z Phi(z) with the normal distribution function, within 1e-7) or silu (z / (1 + e^-z)); pre
+ * gelu (z Phi(z), Phi the normal distribution function within 1.15 2^-20 (1 + z^2 / 8) of its
+ * value, on the left too; below z = -13 the result may be 0) or silu (z / (1 + e^-z)); pre
  * (nullable): z before the activation rounded to `type`, which moe_act_backward takes.
  * The tensor core adds up to 16384 terms (fp16) or 131072 (bf16), truncating, at most about
  * 1/25 of the rounding to 16 bits; longer sums, and binary32 outputs, are joined from partial

@@ -263,3 +263,32 @@ def test_two_streams_and_graphs(dev):
     grads = api.linear_backward(dy, x, w, act="gelu", z=pre, bias=True)
     for y, g in outs:
         assert torch.equal(y, want) and all(torch.equal(g[n], grads[n]) for n in g)
+
+
+def phi(z):
+    """The normal distribution function by erfc, which keeps its digits on the left."""
+    return torch.special.erfc(z * -math.sqrt(0.5)) / 2
+
+
+def normal_distribution_bound(z):
+    """The distribution function's error relative to its value: a quotient and an exponential
+    within 2^-22 (of the quotient's error up to twice arrives), the exponential's argument z^2 / 2
+    in binary32 (2^-23 of 0.6 z^2), 5 roundings, and the fit's 2^-26."""
+    return 1.15 * 2.0 ** -20 * (1 + z * z / 8)
+
+
+def test_gelu_and_its_slope_against_64_bits(dev):
+    """z from the bias alone, so exact in binary32: on the left, where the distribution function is
+    next to nothing, as near to it as elsewhere."""
+    z = torch.cat([torch.linspace(-13, 13, 1 << 17, device=dev), torch.linspace(-0.01, 0.01, 1 << 12, device=dev)])
+    x, w = torch.zeros(1, 8, dtype=BF16, device=dev), torch.zeros(z.numel(), 8, dtype=BF16, device=dev)
+    got = api.linear(x, w, bias=z, act="gelu", out_dtype=F32)[0].double()
+    zd = z.double()
+    want = zd * phi(zd)
+    assert bool(((got - want).abs() <= want.abs() * (normal_distribution_bound(zd) + 2.0 ** -24) + 2.0 ** -118).all())
+    for dtype in (BF16, F16):
+        pre = z.to(dtype)[None]
+        _, slope = api.act_backward(torch.ones_like(pre), pre, "gelu")
+        zd = pre[0].double()
+        cdf, along = phi(zd), zd * torch.exp(-zd * zd / 2) / math.sqrt(2 * math.pi)
+        assert bool(((slope.double() - cdf - along).abs() <= (cdf + along.abs()) * normal_distribution_bound(zd) + 2.0 ** -118).all())
