@@ -996,7 +996,9 @@ class MoELayer:
     follow the routed rows in the row buffers (see moe_layer in include/moe.h).
 
     norm_w fp32 [H]: the layer starts with a root-mean-square norm of its input (rms_norm with
-    these gains and norm_eps), and ``forward`` takes the residual that is added before it.
+    these gains and norm_eps), and ``forward`` takes the residual that is added before it.  Such
+    a layer runs by ``forward`` alone, which can be captured into a graph (torch.cuda.graph);
+    the C layer behind the host-buffer calls and LayerGraph has no norm, so they refuse it.
     """
 
     def __init__(self, cfg: MoEConfig, W_router: torch.Tensor, bias: torch.Tensor | None,
@@ -1119,8 +1121,7 @@ class MoELayer:
 
         A layer with a norm takes x bf16 [B][H] at every call and norms it into self.x;
         ``residual`` (bf16 or fp32 [B][H]) is added to x before, in place: it then holds the
-        sum that the next block adds to.  (The host-buffer calls and a captured graph start
-        behind the norm, at self.x.)
+        sum that the next block adds to.
 
         ``events``: optional list of moe_layer.events torch.cuda.Event recorded at the
         stage boundaries."""
@@ -1152,8 +1153,13 @@ class MoELayer:
             self.layer.events = None
         return self.out
 
+    def _without_norm(self, what: str) -> None:
+        if self.norm_w is not None:
+            raise ValueError(f"{what}: a layer with a norm runs by forward alone (the C layer starts behind the norm)")
+
     def forward_host(self, x_host: torch.Tensor, out_host: torch.Tensor, stream=None) -> None:
         """x from (pinned) host memory, out back to host memory, through the C ABI."""
+        self._without_norm("forward_host")
         check(load().moe_layer_forward_host(ctypes.byref(self.layer), ptr(x_host, host=True),
                                             ptr(out_host, host=True), stream_ptr(stream)),
               "moe_layer_forward_host")
@@ -1163,6 +1169,7 @@ class MoELayer:
         (pinned bf16 [B][H]) in and the output to out_hosts[i] (pinned), the copies of
         neighbouring steps on ``copy_stream`` overlapping the layer on ``stream``.  The
         second pair of device buffers is allocated on first use."""
+        self._without_norm("forward_host_pipelined")
         n = len(x_hosts)
         if n != len(out_hosts) or n < 1:
             raise ValueError("one output buffer per input batch")
@@ -1188,6 +1195,8 @@ class LayerGraph:
 
     def __init__(self, layer: "MoELayer", stream: torch.cuda.Stream,
                  x_host: torch.Tensor | None = None, out_host: torch.Tensor | None = None):
+        self.handle = None
+        layer._without_norm("LayerGraph")
         self._keep = (layer, x_host, out_host)
         h = ctypes.c_void_p()
         check(load().moe_layer_graph_create(ctypes.byref(layer.layer), ptr(x_host, host=True),

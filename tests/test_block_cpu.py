@@ -232,3 +232,13 @@ def test_dense_tile_lists():
     assert api.dense_tiles(0, device="cpu").tolist() == [0] * 8
     with pytest.raises(ValueError):
         api.dense_tiles(-1)
+
+
+def test_a_layer_with_a_norm_refuses_calls_that_would_leave_it_out():
+    lay = object.__new__(api.MoELayer)                            # built by hand: no GPU here
+    lay.norm_w = torch.ones(8)
+    buf = torch.zeros(4, 8, dtype=torch.bfloat16)
+    for call in (lambda: lay.forward_host(buf, buf), lambda: lay.forward_host_pipelined([buf], [buf]),
+                 lambda: api.LayerGraph(lay, None), lambda: api.LayerGraph(lay, None, buf, buf)):
+        with pytest.raises(ValueError, match="norm"):
+            call()

@@ -258,3 +258,29 @@ def test_calls_on_several_streams_at_once(dev):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for j, out in got for a, b in zip(out, want[j]))
     assert api.default_status() == 0
+
+
+def test_the_norm_is_left_out_by_no_call(dev):
+    """What cannot run the norm refuses the layer; forward in a captured graph runs it."""
+    cfg = configs.TINY.with_(B=70)
+    W, _ = inputs.make_router(cfg)
+    gen = torch.Generator("cuda").manual_seed(6)
+    gain = 1 + torch.randn(cfg.H, generator=gen, device=dev) * 0.2
+    lay = api.MoELayer(cfg, torch.from_numpy(W).to(dev), None, layer_weights(cfg, dev)[1], device=dev, norm_w=gain)
+    host = torch.zeros(cfg.B, cfg.H, dtype=BF16).pin_memory()
+    for call in (lambda: lay.forward_host(host, host), lambda: lay.forward_host_pipelined([host], [host]),
+                 lambda: api.LayerGraph(lay, torch.cuda.Stream()), lambda: api.LayerGraph(lay, torch.cuda.Stream(), host, host)):
+        with pytest.raises(ValueError, match="norm"):
+            call()
+    x, res = torch.randn(cfg.B, cfg.H, generator=gen, device=dev).bfloat16(), torch.randn(cfg.B, cfg.H, generator=gen, device=dev)
+    lay.forward(x, residual=res.clone())
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = lay.forward(x, residual=res)
+    for _ in range(2):
+        x.copy_(torch.randn(cfg.B, cfg.H, generator=gen, device=dev))
+        mine = res.clone()
+        g.replay()
+        got = out.clone()
+        assert torch.equal(lay.forward(x, residual=mine), got) and torch.equal(mine, res)
