@@ -535,6 +535,9 @@ Shape shape_of(int H, bool vec, bool few) {
   return s;
 }
 
+// Blocks an SM of the gradients: one kernel more adds up a part of dw each.
+constexpr int kMostGradBlocks = 8;
+
 // The kernels that copy rows ahead: threads with n packs of a row, up to 4 rows ahead, and as
 // many blocks as the SMs hold.  They take over where each block has rows enough to copy ahead,
 // and rows of several warps.
@@ -553,7 +556,7 @@ Ahead ahead_of(int64_t rows, int H, bool vec, int row_bytes, bool grad) {
   a.smem = (uint32_t)(a.stages * row_bytes);
   a.most = std::min(2048 / a.threads, (int)(220u * 1024 / (a.smem + 1024)));
   if (!grad && rows < 4 * (int64_t)device_sm_count()) a.most = 0;
-  if (grad) a.most = std::min(a.most, 8);  // the parts of dw are added up by one kernel more
+  if (grad) a.most = std::min(a.most, kMostGradBlocks);
   return a;
 }
 // Grid of such a kernel: the blocks that are resident, no more than rows.
@@ -638,8 +641,20 @@ bool off(const void *p, int a) { return (uintptr_t)p % a != 0; }
 // Blocks of the backward: each holds the sums of dw of its rows, which a second kernel reads.
 int grad_blocks(int64_t rows, const Shape &s) {
   const int groups = s.block ? 1 : 8;
-  const int64_t need = (rows + groups - 1) / groups, most = (int64_t)device_sm_count() * (!s.block ? 4 : std::max(2, std::min(8, 2048 / s.threads)));
+  const int64_t need = (rows + groups - 1) / groups;
+  const int64_t most = (int64_t)device_sm_count() * (!s.block ? 4 : std::max(2, std::min(kMostGradBlocks, 2048 / s.threads)));
   return (int)(need < most ? need : most);
+}
+// Rows copied ahead by the backward, with dres where three of a row's tensors fit, else without
+// (dres_ahead: which).
+Ahead grad_ahead(int64_t rows, int H, bool vec, int size, bool dres, int *dres_ahead) {
+  Ahead a = ahead_of(rows, H, vec, H * (2 + size * (dres ? 2 : 1)), true);
+  *dres_ahead = dres;
+  if (a.most == 0 && dres) {  // rows too long for three: dres is loaded as it is needed
+    *dres_ahead = 0;
+    a = ahead_of(rows, H, vec, H * (2 + size), true);
+  }
+  return a;
 }
 Shape grad_shape(const moe_norm_grad_args &a) {
   bool vec = a.H % 8 == 0;
@@ -692,9 +707,14 @@ extern "C" int moe_rms_norm(const moe_norm_args *a, void *stream) {
 
 extern "C" size_t moe_rms_norm_workspace_size(const moe_norm_grad_args *a) {
   if (!a || check_norm(a->rows, a->H, a->eps, a->type, a->res_type) != MOE_OK || a->rows == 0) return 0;
-  // the most blocks that any alignment of the tensors asks for
-  int most = a->H >= 256 ? (int)std::min<int64_t>(a->rows, (int64_t)device_sm_count() * 32) : 0;
-  for (bool vec : {true, false}) most = std::max(most, grad_blocks(a->rows, shape_of(a->H, vec, false)));
+  // the most blocks that any alignment of the tensors asks for, with dres or without
+  int most = grad_blocks(a->rows, shape_of(a->H, false, false)), ahead;
+  for (bool dres : {true, false}) {
+    if (a->H % 8) break;
+    const Ahead s = grad_ahead(a->rows, a->H, true, a->res_type == MOE_TYPE_F32 ? 4 : 2, dres, &ahead);
+    most = std::max(most, s.most > 0 ? (int)std::min<int64_t>(a->rows, (int64_t)device_sm_count() * s.most)
+                                     : grad_blocks(a->rows, shape_of(a->H, true, false)));
+  }
   return (size_t)most * a->H * sizeof(float);
 }
 
@@ -717,12 +737,8 @@ extern "C" int moe_rms_norm_backward(const moe_norm_grad_args *a, void *workspac
   const Shape s = grad_shape(*a);
   int blocks = grad_blocks(a->rows, s);
   NormGradParams P = {a->rows, a->H, a->eps, 1.0f / a->H, a->h, a->dy, a->dres, a->w, a->dx,
-                      a->dw ? static_cast<float *>(workspace) : nullptr, a->dres != nullptr};
-  Ahead ahead = ahead_of(a->rows, a->H, s.V == 8, a->H * (2 + size * (a->dres ? 2 : 1)), true);
-  if (ahead.most == 0 && a->dres) {  // rows too long for three: dres is loaded as it is needed
-    P.dres_ahead = 0;
-    ahead = ahead_of(a->rows, a->H, s.V == 8, a->H * (2 + size), true);
-  }
+                      a->dw ? static_cast<float *>(workspace) : nullptr, 0};
+  const Ahead ahead = grad_ahead(a->rows, a->H, s.V == 8, size, a->dres != nullptr, &P.dres_ahead);
   const int done = ahead.most > 0 ? with_ahead<true>(a->type, a->res_type, ahead, [&](auto t, auto r, auto n, auto stages, auto bound) {
     constexpr auto kernel = norm_grad_rows_kernel<decltype(t), decltype(r), decltype(n)::value, decltype(stages)::value,
                                             decltype(bound)::value>;

@@ -242,3 +242,11 @@ def test_a_layer_with_a_norm_refuses_calls_that_would_leave_it_out():
                  lambda: api.LayerGraph(lay, None), lambda: api.LayerGraph(lay, None, buf, buf)):
         with pytest.raises(ValueError, match="norm"):
             call()
+
+
+@pytest.mark.parametrize("rows,H,res_type", [(8192, 7168, 0), (8192, 7168, 2), (100000, 16384, 0), (3, 16384, 2), (50, 512, 0),
+                                             (9000, 1001, 2), (9000, 100, 0), (1, 1, 0)])
+def test_norm_workspace_is_what_the_parts_take(L, rows, H, res_type):
+    """A part of dw a block, and at most 8 blocks an SM."""
+    size = L.moe_rms_norm_workspace_size(ctypes.byref(make(_lib.NormGradArgs, rows=rows, H=H, eps=1e-6, type=0, res_type=res_type)))
+    assert 4 * H <= size <= 4 * H * min(rows, 8 * L.moe_num_sms())
