@@ -527,11 +527,7 @@ Shape shape_of(int H, bool vec, bool few) {
     return s;
   }
   s.n = vec ? (few && packs <= 1024 ? 1 : few ? 2 : 4) : (packs <= 4096 ? 4 : 16);
-  s.threads = ((packs + s.n - 1) / s.n + 31) / 32 * 32;
-  if (s.threads > 1024) {
-    s.n = most;
-    s.threads = ((packs + s.n - 1) / s.n + 31) / 32 * 32;
-  }
+  s.threads = ((packs + s.n - 1) / s.n + 31) / 32 * 32;  // kMaxH takes 1024 at most
   return s;
 }
 
@@ -586,8 +582,9 @@ int check_norm(int64_t rows, int H, float eps, int type, int res_type) {
   return MOE_OK;
 }
 
-// Calls f with the types and the shape as constants.
-template <class F>
+// Calls f with the types and the shape as constants: of the gradients (kGrad) whole vectors only
+// where no rows are copied ahead, rows below 256 columns and those of binary32 past 12456.
+template <bool kGrad, class F>
 int with_shape(int type, int res_type, const Shape &s, F f) {
   auto shaped = [&](auto t, auto r) {
     using std::integral_constant;
@@ -596,16 +593,22 @@ int with_shape(int type, int res_type, const Shape &s, F f) {
     const integral_constant<int, 8> v8;
     const integral_constant<int, 1> v1;
     const integral_constant<int, 1> n1;
-    const integral_constant<int, 2> n2;
+    [[maybe_unused]] const integral_constant<int, 2> n2;
     const integral_constant<int, 4> n4;
     const integral_constant<int, 16> n16;
     if (s.V == 1) {
       if (s.n == 4) return f(t, r, v1, n4, block);
       return s.block ? f(t, r, v1, n16, block) : f(t, r, v1, n16, warp);
     }
-    if (s.n == 1) return s.block ? f(t, r, v8, n1, block) : f(t, r, v8, n1, warp);
-    if (s.n == 2) return s.block ? f(t, r, v8, n2, block) : f(t, r, v8, n2, warp);
-    return s.block ? f(t, r, v8, n4, block) : f(t, r, v8, n4, warp);
+    if constexpr (kGrad) {
+      if constexpr (std::is_same<decltype(r), float>::value)
+        if (s.block) return f(t, r, v8, n4, block);
+      return f(t, r, v8, n1, warp);
+    } else {
+      if (s.n == 1) return s.block ? f(t, r, v8, n1, block) : f(t, r, v8, n1, warp);
+      if (s.n == 2) return s.block ? f(t, r, v8, n2, block) : f(t, r, v8, n2, warp);
+      return s.block ? f(t, r, v8, n4, block) : f(t, r, v8, n4, warp);
+    }
   };
   if (type == MOE_TYPE_BF16)
     return res_type == MOE_TYPE_F32 ? shaped(__nv_bfloat16(), float()) : shaped(__nv_bfloat16(), __nv_bfloat16());
@@ -625,7 +628,9 @@ int with_ahead(int type, int res_type, const Ahead &a, F f) {
     if constexpr (kGrad) {
       if (a.n == 1) return f(t, r, one, four, b512);  // rows of up to 20 KB
       if (a.threads > 512) return a.stages == 4 ? f(t, r, two, four, b1024) : f(t, r, two, three, b1024);
-      return a.stages == 4 ? f(t, r, two, four, b512) : f(t, r, two, three, b512);
+      if constexpr (std::is_same<decltype(r), float>::value)  // 16-bit rows this short leave room for 4
+        if (a.stages == 3) return f(t, r, two, three, b512);
+      return f(t, r, two, four, b512);
     } else {
       if (a.n == 4) return f(t, r, four, two, b512);
       return a.stages == 4 ? f(t, r, two, four, b512) : f(t, r, two, two, b512);
@@ -697,7 +702,7 @@ extern "C" int moe_rms_norm(const moe_norm_args *a, void *stream) {
       return check_launch();
     });
   const Shape s = shape_of(a->H, vec, a->rows <= 2 * device_sm_count());
-  return with_shape(a->type, a->res_type, s, [&](auto t, auto r, auto v, auto n, auto block) {
+  return with_shape<false>(a->type, a->res_type, s, [&](auto t, auto r, auto v, auto n, auto block) {
     const unsigned grid = (unsigned)(s.block ? a->rows : (a->rows + 7) / 8);
     norm_kernel<decltype(t), decltype(r), v.value, n.value, block.value>
         <<<grid, s.block ? s.threads : 256, 0, as_stream(stream)>>>(P);
@@ -746,7 +751,7 @@ extern "C" int moe_rms_norm_backward(const moe_norm_grad_args *a, void *workspac
     if (found != MOE_OK) return found;
     kernel<<<blocks, ahead.threads, ahead.smem, st>>>(P);
     return check_launch();
-  }) : with_shape(a->type, a->res_type, s, [&](auto t, auto r, auto v, auto n, auto block) {
+  }) : with_shape<true>(a->type, a->res_type, s, [&](auto t, auto r, auto v, auto n, auto block) {
     const size_t smem = s.block || !a->dw ? 0 : sizeof(float) * a->H;
     norm_grad_kernel<decltype(t), decltype(r), v.value, n.value, block.value>
         <<<blocks, s.block ? s.threads : 256, smem, st>>>(P);
