@@ -12,6 +12,7 @@
 #include <cuda_fp16.h>
 #include <float.h>
 
+#include <mutex>
 #include <type_traits>
 
 #include "common.cuh"
@@ -1290,6 +1291,44 @@ int with_type(int type, F f) {
   if (type == MOE_TYPE_F32) return f(float());
   return type == MOE_TYPE_F16 ? f(__half()) : f(__nv_bfloat16());
 }
+cudaLaunchConfig_t one_cluster(int blocks, cudaLaunchAttribute *attr, cudaStream_t st) {
+  cudaLaunchConfig_t launch = {};
+  launch.gridDim = dim3((unsigned)blocks);
+  launch.blockDim = dim3(kWarps * 32);
+  launch.stream = st;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = (unsigned)blocks;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
+  launch.attrs = attr;
+  launch.numAttrs = 1;
+  return launch;
+}
+// Blocks of the largest cluster of this kernel that the device runs: 16 where its processors come
+// in groups of enough, else half of that and so on.  Asked once a device.
+template <auto kernel>
+int largest_cluster(int *most) {
+  static int sizes[kMaxDevices] = {};
+  static std::mutex asked;
+  const int dev = device_slot();
+  if (dev < 0) return dev;
+  const std::lock_guard<std::mutex> lock(asked);
+  if (sizes[dev] == 0) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return set_cuda_error(e);
+    int size = kClusterTokens / kWarps;
+    for (; size > 1; size /= 2) {
+      cudaLaunchAttribute attr;
+      const cudaLaunchConfig_t launch = one_cluster(size, &attr, nullptr);
+      int fit = 0;
+      if (cudaOccupancyMaxActiveClusters(&fit, kernel, &launch) == cudaSuccess && fit > 0) break;
+      cudaGetLastError();  // a size that the device does not take
+    }
+    sizes[dev] = size;
+  }
+  *most = sizes[dev];
+  return MOE_OK;
+}
 unsigned grid_of(int64_t B) {
   const int64_t need = (B + kWarps - 1) / kWarps, most = (int64_t)device_sm_count() * 32;
   return (unsigned)(need < most ? need : most);
@@ -1343,33 +1382,24 @@ extern "C" int moe_route_topk(const moe_route_cfg *cfg, int type, const void *lo
   // A cluster of up to 16 blocks needs no counts set to zero (3.5 us), as long as a warp has one
   // token (128 tokens on 8 blocks: 13 us; 11 with counts set to zero).
   const int64_t blocks = (cfg->B + kWarps - 1) / kWarps;
-  const bool cluster = expert_counts && blocks <= kClusterTokens / kWarps;
-  if (!cluster) {
-    const int cleared = zero();
-    if (cleared != MOE_OK) return cleared;
-  }
   return with_type(type, [&](auto t) {
     return with_npl(npl, [&](auto n) {
-      if (!cluster) {
-        route_topk_kernel<decltype(t), n.value, false><<<grid_of(cfg->B), kWarps * 32, 0, st>>>(P);
-        return check_launch();
+      if (expert_counts && blocks <= kClusterTokens / kWarps) {
+        constexpr auto kernel = route_topk_kernel<decltype(t), decltype(n)::value, true>;
+        int most = 0;
+        const int found = largest_cluster<kernel>(&most);
+        if (found != MOE_OK) return found;
+        if (blocks <= most) {
+          cudaLaunchAttribute attr;
+          const cudaLaunchConfig_t launch = one_cluster((int)blocks, &attr, st);
+          const cudaError_t e = cudaLaunchKernelEx(&launch, kernel, P);
+          return e == cudaSuccess ? check_launch() : set_cuda_error(e);
+        }
       }
-      cudaLaunchConfig_t launch = {};
-      launch.gridDim = dim3((unsigned)blocks);
-      launch.blockDim = dim3(kWarps * 32);
-      launch.stream = st;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = launch.gridDim.x;
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      launch.attrs = attr;
-      launch.numAttrs = 1;
-      constexpr auto kernel = route_topk_kernel<decltype(t), decltype(n)::value, true>;
-      cudaError_t e = cudaSuccess;
-      if (blocks > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-      if (e == cudaSuccess) e = cudaLaunchKernelEx(&launch, kernel, P);
-      return e == cudaSuccess ? check_launch() : set_cuda_error(e);
+      const int cleared = zero();
+      if (cleared != MOE_OK) return cleared;
+      route_topk_kernel<decltype(t), n.value, false><<<grid_of(cfg->B), kWarps * 32, 0, st>>>(P);
+      return check_launch();
     });
   });
 }
