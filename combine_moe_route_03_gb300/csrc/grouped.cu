@@ -59,6 +59,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <mutex>
 #include <type_traits>
 
 #include "entry.cuh"
@@ -1043,6 +1044,7 @@ int check_common(const moe_segments &seg, int n, int k, int type, bool all_rows 
 template <int kMode, class O, bool kLong = false>
 int launch(const Maps &maps, const GroupedParams &P, int64_t max_units, int num_sms, void *stream) {
   static int max_clusters[kMaxDevices] = {};
+  static std::mutex asked;  // threads whose first calls come at once
   const int dev = device_slot();
   if (dev < 0) return dev;
   auto kernel = grouped_kernel<kMode, O, kLong>;
@@ -1060,6 +1062,7 @@ int launch(const Maps &maps, const GroupedParams &P, int64_t max_units, int num_
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  std::unique_lock<std::mutex> lock(asked);
   if (max_clusters[dev] == 0) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kSmem);
@@ -1071,6 +1074,7 @@ int launch(const Maps &maps, const GroupedParams &P, int64_t max_units, int num_
   }
   int64_t clusters = cfg.gridDim.x / 2;
   if (clusters > max_clusters[dev]) clusters = max_clusters[dev];
+  lock.unlock();
   if (clusters > max_units) clusters = max_units;
   if (clusters < 1) return MOE_OK;
   cfg.gridDim = dim3((unsigned)(2 * clusters));

@@ -544,8 +544,10 @@ cudaLaunchConfig_t config(int ctas, int splits, cudaLaunchAttribute *attr, void 
 template <auto kernel>
 int prepare() {
   static bool done[kMaxDevices] = {};
+  static std::mutex setting;  // threads whose first calls come at once
   const int dev = device_slot();
   if (dev < 0) return dev;
+  const std::lock_guard<std::mutex> lock(setting);
   if (!done[dev]) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);

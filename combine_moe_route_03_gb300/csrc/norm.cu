@@ -10,6 +10,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <mutex>
 #include <type_traits>
 
 #include "columns.cuh"
@@ -559,8 +560,10 @@ Ahead ahead_of(int64_t rows, int H, bool vec, int row_bytes, bool grad) {
 template <auto kernel>
 int resident(const Ahead &a, int64_t rows, int *grid) {
   static int regs[kMaxDevices] = {};
+  static std::mutex asked;  // threads whose first calls come at once
   const int dev = device_slot();
   if (dev < 0) return dev;
+  const std::lock_guard<std::mutex> lock(asked);
   if (regs[dev] == 0) {
     cudaFuncAttributes at;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);

@@ -4,6 +4,7 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -124,14 +125,15 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
+  static std::atomic<EncodeTiledFn> known{nullptr};  // threads may ask at once
+  EncodeTiledFn fn = known.load();
   if (!fn) {
     void *p = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
                                          &q) == cudaSuccess &&
         q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
+      known.store(fn = reinterpret_cast<EncodeTiledFn>(p));
   }
   return fn;
 }

@@ -284,3 +284,39 @@ def test_the_norm_is_left_out_by_no_call(dev):
         g.replay()
         got = out.clone()
         assert torch.equal(lay.forward(x, residual=mine), got) and torch.equal(mine, res)
+
+
+FIRST_CALLS = """
+import threading, torch
+from combine_moe_route_03_gb300 import api, configs
+gen = torch.Generator("cuda").manual_seed(0)
+rand = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()
+x, w, dy, h, gain = rand(700, 512), rand(264, 512), rand(700, 264), rand(700, 2048), torch.ones(2048, device="cuda")
+z = torch.randn(100, 64, generator=gen, device="cuda")
+cfg = configs.MoEConfig("routing", B=100, H=128, N=64, K=4, I=128)
+def calls():
+    b = api.linear_backward(dy, x, w, act="silu", z=dy)
+    return [api.linear(x, w), api.linear(x[:8], w, out_dtype=torch.float32), b["dx"], b["dw"], api.rms_norm(h, gain)["y"],
+            *api.rms_norm_backward(h, gain, h), *api.route_topk(cfg, z).values()]
+torch.cuda.synchronize()
+gate, got = threading.Barrier(8), [None] * 8
+def go(i):
+    gate.wait()
+    got[i] = calls()
+threads = [threading.Thread(target=go, args=(i,)) for i in range(8)]
+for t in threads: t.start()
+for t in threads: t.join()
+want = calls()
+assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+print("the same")
+"""
+
+
+def test_first_calls_of_several_threads_at_once(dev):
+    """What a process asks of a device once is asked by all of them."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "the same" in run.stdout, run.stderr[-2000:]
