@@ -644,7 +644,7 @@ extern "C" int moe_linear(const moe_linear_args *a, void *stream) {
   P.q_tiles = plan.q_tiles;
   P.p_tiles = plan.p_tiles;
   // as many rows of x as columns of w in the units side by side
-  P.band = std::max(1, (int)std::lround(std::sqrt((double)(sms / 2) * BP / plan.nq)));
+  P.band = std::max(1, (int)std::lround(std::sqrt((double)pairs * BP / plan.nq)));
   P.units = (int)units;
   P.splits = plan.splits;
   P.chunk = f32 ? kSumBlocks : longer ? kJoinBlocks : P.blocks;

@@ -292,3 +292,13 @@ def test_gelu_and_its_slope_against_64_bits(dev):
         zd = pre[0].double()
         cdf, along = phi(zd), zd * torch.exp(-zd * zd / 2) / math.sqrt(2 * math.pi)
         assert bool(((slope.double() - cdf - along).abs() <= (cdf + along.abs()) * normal_distribution_bound(zd) + 2.0 ** -118).all())
+
+
+def test_more_sms_asked_for_than_there_are(dev):
+    """The grid and the units' order go by what the device has, also for millions of columns."""
+    gen = torch.Generator("cuda").manual_seed(8)
+    x, w = normal(gen, 40, 8), normal(gen, 6_100_000, 8)
+    want = api.linear(x, w)
+    assert torch.equal(api.linear(x, w, num_sms_=2 ** 31 - 1), want)
+    z, slack = reference(x, w[-300:], None, False, BF16)
+    check_close(want[:, -300:].contiguous(), z, slack, BF16)
