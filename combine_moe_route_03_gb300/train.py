@@ -177,6 +177,11 @@ class LayerTrainer:
         if self._saved is None:
             raise ValueError("backward: a forward before it expected")
         y, h, logits, topk_idx, shared = self._saved
+        # before anything is added to a gradient
+        api._is(dout, "dout", torch.bfloat16, h.shape)
+        if dh is not None:
+            api._is(dh, "dh", h.dtype, h.shape)
+        _lib.ptrs(dout, dh)
         self._saved = None
         more = dict(accumulate=not self.experts._fresh)
         dy, dw = self.experts.backward(dout)

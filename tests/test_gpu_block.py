@@ -320,3 +320,22 @@ def test_first_calls_of_several_threads_at_once(dev):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     run = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
     assert run.returncode == 0 and "the same" in run.stdout, run.stderr[-2000:]
+
+
+def test_a_refused_backward_leaves_the_gradients_alone(dev):
+    """What backward cannot take is refused before anything is added up: the right call after it
+    gives what it gives alone."""
+    params, r = parameters(SMALL, 3)
+    t, fresh = (train.LayerTrainer(SMALL, *params) for _ in range(2))
+    x, res = r(SMALL.B, SMALL.H).bfloat16(), r(SMALL.B, SMALL.H)
+    dout, dh = r(SMALL.B, SMALL.H).bfloat16(), r(SMALL.B, SMALL.H)
+    for u in (t, fresh):
+        u.forward(x, res)
+    for bad in (dict(dh=dh.bfloat16()), dict(dh=dh[:-1]), dict(dh=dh.t().contiguous().t()), dict(dh=dh.cpu()), dict(dout=dout.float()),
+                dict(dout=dout[1:]), dict(dout=dout.cpu())):
+        with pytest.raises(ValueError):
+            t.backward(**{**dict(dout=dout, dh=dh), **bad})
+        assert not any(bool(g.any()) for g in (*t.grads, *t.experts.grads))
+    assert torch.equal(t.backward(dout, dh), fresh.backward(dout, dh))
+    for got, want in zip((*t.grads, *t.experts.grads), (*fresh.grads, *fresh.experts.grads)):
+        assert torch.equal(got, want)
