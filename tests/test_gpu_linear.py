@@ -302,3 +302,48 @@ def test_more_sms_asked_for_than_there_are(dev):
     assert torch.equal(api.linear(x, w, num_sms_=2 ** 31 - 1), want)
     z, slack = reference(x, w[-300:], None, False, BF16)
     check_close(want[:, -300:].contiguous(), z, slack, BF16)
+
+
+def off(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("rows,n,k,trans", [(128, 256, 7168, False), (1, 4096, 7168, False), (2500, 264, 7168, False),
+                                            (8192, 256, 7168, False), (128, 7168, 256, True), (1500, 7168, 520, True)])
+def test_binary32_outputs_hold_more_than_16_bits(dev, rows, n, k, trans, dtype):
+    """Relative 2-norm of the error of sums of 7168 random terms, split over a cluster or not.  An
+    instruction adds 16 products and drops what is below the last of the sum's 24 bits, 0.36 2^-23 of the
+    sum on average, towards zero.  For terms of size 1 the 32 drops of a partial sum of 512 add up to at
+    most 0.36 2^-23 sum_j 4 sqrt(j) = 2.1e-5, those of 14 partial sums, of either sign, to 7.8e-5 of
+    84.7, 9.2e-7; the roundings of 14 additions to less than 1e-7 of it in squares.  One sum of all 448
+    instructions would lose 11 times as much, an output rounded to 16 bits 200 times."""
+    gen = torch.Generator("cuda").manual_seed(rows)
+    red = n if trans else k
+    x, w = normal(gen, rows, red, dtype=dtype), normal(gen, n, k, dtype=dtype, scale=red ** -0.5)
+    got = api.linear(x, w, trans=trans, out_dtype=F32)
+    assert off(got, x.double() @ (w.double() if trans else w.double().t())) <= 1e-6
+
+
+@pytest.mark.parametrize("dtype,red", [(F16, 16384 + 72), (BF16, 131072 + 8)])
+@pytest.mark.parametrize("rows", [3, 300])
+def test_long_sums_of_positive_terms(dev, dtype, red, rows):
+    """Truncations of positive terms all add up.  Binary32 outputs: in a part of 512 terms 32
+    truncations of at most 2^-22 of a sum that grows evenly, and a rounding (2^-24) a joined
+    part of a sum that does: below what one sum of all terms loses, 0.18 2^-23 of it an
+    instruction.  16-bit outputs, four times as long: parts of 4096 terms, seen in the mean over many
+    outputs, whose own roundings cancel there."""
+    gen = torch.Generator("cuda").manual_seed(rows)
+    make = lambda r: (normal(gen, rows, r, dtype=dtype).abs(), (normal(gen, 40, r, dtype=dtype).abs() * r ** -0.5).to(dtype))  # noqa: E731
+    x, w = make(red)
+    z = x.double() @ w.double().t()
+    bound = 17 * 2.0 ** -22 + (red // 512 + 2) / 2 * 2.0 ** -24
+    assert bound < 0.18 * 2.0 ** -23 * red / 16
+    assert bool(((api.linear(x, w, out_dtype=F32).double() - z).abs() <= z * bound).all())
+    x, w = make(4 * red)
+    z = x.double() @ w.double().t()
+    half = 2.0 ** -11 if dtype == F16 else 2.0 ** -8
+    bound = 129 * 2.0 ** -22 + 5 * half / (3 * z.numel()) ** 0.5 + (red // 1024 + 2) / 2 * 2.0 ** -24
+    if rows == 300:
+        assert bound < 0.18 * 2.0 ** -23 * red / 4
+    assert abs(float((api.linear(x, w).double() / z - 1).mean())) <= bound
