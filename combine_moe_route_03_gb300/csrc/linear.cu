@@ -9,7 +9,7 @@
 // each CTA with 128 of the tile's p and half of its q.  A unit of work is 256 p and up to 256 q,
 // one accumulator; the other takes the next unit's MMAs while this one's is stored.  (Units of
 // 512 q on both read the P tile once for the two, but nothing runs beside their stores: 8192 x
-// 7168 x 2048 156 us against 127; 8192 x 4096 x 7168 306 and 271.)
+// 7168 x 2048 took 156 us so, 131 now; 8192 x 4096 x 7168 306 and 262.)
 //   warp 0  producer: TMA tiles into a ring in shared memory
 //   warp 1  MMA issuer (of the even CTA) and TMEM owner
 //   warps 4-19  epilogue: TMEM -> registers -> global (with 8 warps it took longer than the
@@ -100,7 +100,7 @@ __device__ __forceinline__ uint32_t pack2f(float a, float b, __nv_bfloat16) {
 // straight from registers; the swap is its own inverse, which brings the residual back.  The
 // extent of p is a multiple of 8, so a pair is inside or outside as one.
 // What is read or written once is marked so, and leaves the L2 to the operands (8192 x 7168 x
-// 2048 with residual: 139 -> 138 us; the residual asked for a unit ahead: 144).
+// 2048 with residual: 139 -> 138 us, 140 in later runs; the residual asked for a unit ahead: 144).
 // kAhead q's of the residual are asked for at a time: all, or fewer where the registers hold
 // sums besides.
 template <class T, class O, int kAhead>
